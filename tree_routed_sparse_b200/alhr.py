@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libalhr.so (the C ABI declared in include/alhr.h).
+"""Thin ctypes binding of libalhr.so (the C ABI declared in include/alhr.h; that of
+include/alhr_cache.h is bound in cache.py).
 
 Argument marshalling only: shapes are read from the torch tensors, outputs are allocated with
 torch on the inputs' device, raw pointers and the current CUDA stream are passed to the C entry
@@ -29,7 +30,10 @@ EXPORTS = ["alhr_tree_rows", "alhr_tree_narrow_levels", "alhr_tree_bytes",
            "alhr_tree_level_offset", "alhr_score_bits", "alhr_status_string", "alhr_build_info",
            "alhr_build_tree", "alhr_update_tree", "alhr_tree_unpack", "alhr_predict_budget",
            "alhr_route", "alhr_attend", "alhr_forward", "alhr_set_launch_mode",
-           "alhr_get_launch_mode", "alhr_topk_labels", "alhr_tree_pack"]
+           "alhr_get_launch_mode", "alhr_topk_labels", "alhr_tree_pack",
+           # include/alhr_cache.h, bound in cache.py
+           "alhr_plan_blocks", "alhr_store_cache", "alhr_load_cache",
+           "alhr_attend_cache_workspace", "alhr_attend_cache", "alhr_attend_cache_selected"]
 
 
 class AlhrError(RuntimeError):
@@ -77,9 +81,19 @@ def lib() -> ctypes.CDLL:
         L.alhr_topk_labels.argtypes = [DP, P, P, I32, P, P, P, P]
         L.alhr_set_launch_mode.argtypes = [I32]
         L.alhr_get_launch_mode.argtypes, L.alhr_get_launch_mode.restype = [], I32
+        I64 = ctypes.c_int64
+        L.alhr_plan_blocks.argtypes = [I32] * 6 + [P] * 12
+        L.alhr_store_cache.argtypes = [P, P, P, I32, I32, I64, I64, I64, I64, P, P, P]
+        L.alhr_load_cache.argtypes = [P, P, P, I32, I32, P, P, P]
+        L.alhr_attend_cache_workspace.argtypes = [P, P]
+        L.alhr_attend_cache_workspace.restype = SZ
+        L.alhr_attend_cache.argtypes = [P] * 10 + [SZ, P, P]
+        L.alhr_attend_cache_selected.argtypes = [P] * 11
         for f in ("alhr_build_tree", "alhr_update_tree", "alhr_tree_unpack", "alhr_tree_pack",
                   "alhr_predict_budget", "alhr_route", "alhr_attend", "alhr_forward",
-                  "alhr_set_launch_mode", "alhr_topk_labels"):
+                  "alhr_set_launch_mode", "alhr_topk_labels", "alhr_plan_blocks",
+                  "alhr_store_cache", "alhr_load_cache", "alhr_attend_cache",
+                  "alhr_attend_cache_selected"):
             getattr(L, f).restype = I32
         _lib = L
     return _lib

@@ -2,7 +2,7 @@
 
     python -m tree_routed_sparse_b200.build [--force] [--verbose-ptxas]
 
-The library is rebuilt when the hash of its sources (csrc/*, include/alhr.h, this file)
+The library is rebuilt when the hash of its sources (csrc/*, include/*.h, this file)
 changes; the hash is kept beside the library.
 """
 from __future__ import annotations
@@ -36,7 +36,7 @@ def sources() -> list[str]:
 def _hash() -> str:
     h = hashlib.sha1()
     files = sorted(glob.glob(os.path.join(PKG, "csrc", "*"))) + [
-        os.path.join(ROOT, "include", "alhr.h"), os.path.abspath(__file__)]
+        *sorted(glob.glob(os.path.join(ROOT, "include", "*.h"))), os.path.abspath(__file__)]
     for f in files:
         h.update(os.path.basename(f).encode())
         with open(f, "rb") as fh:
@@ -84,7 +84,8 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
         return LIB
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [NVCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, *sources()]
+    # -t 0: the files are compiled side by side (what is compiled does not depend on it)
+    cmd = [NVCC, "-t", "0", *FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, *sources()]
     if ptxas_verbose:
         cmd.insert(1, "-Xptxas=-v")
     subprocess.run(cmd, check=True)

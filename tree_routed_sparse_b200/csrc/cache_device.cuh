@@ -1,0 +1,71 @@
+// cache_device.cuh -- device building blocks of the paged 8-bit cache.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "cache_internal.h"
+
+namespace alhr {
+
+// First code row of (block, head); rows are below 2^31 (checked on the host), bytes are not.
+__device__ __forceinline__ long long block_row(const CacheView& c, int block, int head) {
+  return (static_cast<long long>(block) * c.heads + head) << c.bs_log;
+}
+
+__device__ __forceinline__ void cache_flag(uint32_t* dev_err, uint32_t bit) {
+  if (dev_err) atomicOr(dev_err, bit);
+}
+
+// Code <-> number. CODE is an alhr_code.
+template <int CODE>
+__device__ __forceinline__ float decode(uint8_t c) {
+  if constexpr (CODE == ALHR_CODE_INT8) return static_cast<float>(static_cast<int8_t>(c));
+  else return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+}
+
+template <int CODE>
+__device__ __forceinline__ uint8_t encode(float x) {  // to nearest even, saturated; NaN as 0
+  if (x != x) return 0;
+  if constexpr (CODE == ALHR_CODE_INT8)
+    return static_cast<uint8_t>(__float2int_rn(fminf(fmaxf(x, -127.f), 127.f)));
+  else
+    return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+}
+
+// Eight consecutive numbers of type T (an alhr_type) as fp32.
+template <int T>
+__device__ __forceinline__ void unpack8(const uint4& a, const uint4& b, float (&x)[8]) {
+  if constexpr (T == ALHR_TYPE_FP32) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+  } else {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (T == ALHR_TYPE_BF16) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, bool fp16) {
+  if (fp16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+}  // namespace alhr
