@@ -104,13 +104,17 @@ def score_error(d, most):
 
 def attend_ref(q, k, v, kscale, vscale, table, ctx, seq, q_start, scale, k_all=None):
     """alhr_attend_cache in 64 bits. Returns out, lse, weight (sum p |v|: what a relative error of
-    the weights can move), most (|q| . |k| * scale) and which rows belong to a request."""
+    the weights can move), most (|q| . |k| * scale), which rows belong to a request and small:
+    what an absolute error of 1 in every weight can move, for weights 2^(x_j - M),
+    x_j = log2(exp(s_j) vscale_j), that multiply codes and of which the largest is at least 1:
+    sum |code_j| / l with l = sum 2^(x_j - M) / vscale_j >= 1 / vscale_top, so that
+    small = vscale_top sum |code_j|."""
     T, hq, d = q.shape
     blocks, hkv, bs, _ = k.shape
     width, g = table.shape[1], hq // hkv
     dev = q.device
     out = torch.zeros(T, hq, d, dtype=torch.float64, device=dev)
-    weight = torch.zeros_like(out)
+    weight, small = torch.zeros_like(out), torch.zeros_like(out)
     lse = torch.full((T, hq), -math.inf, dtype=torch.float64, device=dev)
     owned = torch.zeros(T, dtype=torch.bool)
     most = 0.0
@@ -128,6 +132,8 @@ def attend_ref(q, k, v, kscale, vscale, table, ctx, seq, q_start, scale, k_all=N
         pages = pages.clamp(0, blocks - 1)
         take = lambda x, s: numbers(x[pages], s[pages]).transpose(0, 1).reshape(hkv, -1, d)[:, :n]
         K, V = take(k, kscale), take(v, vscale)
+        codes = torch.nan_to_num(take(v, torch.ones_like(vscale))).abs()
+        vs = vscale[pages].double().T.repeat_interleave(bs, 1)[:, :n].clamp(min=TINY)
         pos = ctx[r] + torch.arange(hi - lo, device=dev)
         seen = (torch.arange(n, device=dev)[None] <= pos[:, None]) & ok[None]
         for h in range(hkv):
@@ -141,7 +147,10 @@ def attend_ref(q, k, v, kscale, vscale, table, ctx, seq, q_start, scale, k_all=N
             out[lo:hi, h * g:(h + 1) * g] = p @ torch.nan_to_num(V[h])
             weight[lo:hi, h * g:(h + 1) * g] = p @ torch.nan_to_num(V[h]).abs()
             lse[lo:hi, h * g:(h + 1) * g] = l
-    return out, lse, weight, most, owned
+            top = vs[h][(s + vs[h].log()).argmax(-1)]
+            small[lo:hi, h * g:(h + 1) * g] = top[..., None] * (
+                seen.double() @ codes[h])[:, None]
+    return out, lse, weight, most, owned, small
 
 
 def random_cache(blocks, hkv, bs, d, dtype, g, dev, spread=0.4):

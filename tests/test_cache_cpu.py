@@ -198,7 +198,7 @@ def test_attention_by_hand():
     q = torch.zeros(1, 1, 64)
     q[0, 0, 0] = 1.0
     i = lambda *x: torch.tensor(x, dtype=torch.int32)
-    out, lse, _, _, owned = attend_ref(q, k, v, one, half, i(1)[None], i(1), i(9), i(0, 1), 1.0)
+    out, lse, _, _, owned, _ = attend_ref(q, k, v, one, half, i(1)[None], i(1), i(9), i(0, 1), 1.0)
     e1, e2 = math.exp(1), math.exp(2)
     assert abs(out[0, 0, 5].item() - 0.5 * (10 * e1 + 20 * e2) / (e1 + e2)) < 1e-12
     assert abs(lse.item() - math.log(e1 + e2)) < 1e-12 and owned.tolist() == [True]
@@ -215,7 +215,7 @@ def test_attend_ref_sees_planted_mistakes():
     q = 2 * torch.randn(1, 2, 64, generator=g)
     run = lambda ctx=40, ks=c["k_scale"], vs=c["v_scale"]: attend_ref(
         q, c["k"], c["v"], ks, vs, i(2, 0, 3)[None], i(ctx), i(48), i(0, 1), 0.125)
-    ref, _, weight, most, _ = run()
+    ref, _, weight, most, *_ = run()
     tol = 2.0 ** -8 * ref.abs() + (2.0 ** -11 + 2 * score_error(64, most)) * weight
     for other in (run(ctx=39), run(ctx=41), run(ks=c["k_scale"].mean().expand(4, 1)),
                   run(vs=c["v_scale"].mean().expand(4, 1))):

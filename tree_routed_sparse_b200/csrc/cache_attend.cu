@@ -46,49 +46,6 @@ struct Row {
 };
 
 template <int D, int CODE>
-__global__ void __launch_bounds__(kRowWarps * 32) attend_rows_kernel(const AttendArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long rows = static_cast<long long>(a.tokens) * a.q_heads;
-  for (long long u = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5); u < rows;
-       u += static_cast<long long>(gridDim.x) * kRowWarps) {
-    const int t = static_cast<int>(u / a.q_heads), h = static_cast<int>(u - (long long)t * a.q_heads);
-    int r = -1, first = 0;  // the request of row t
-    for (int i = lane; i < a.requests; i += 32) {
-      const int lo = max(__ldg(a.q_start + i), 0), hi = min(__ldg(a.q_start + i + 1), a.tokens);
-      if (lo <= t && t < hi) { r = i; first = lo; }
-    }
-    r = __reduce_max_sync(0xffffffffu, r);
-    first = __reduce_max_sync(0xffffffffu, first);
-    if (r < 0) continue;
-    const long long cap = static_cast<long long>(a.max_blocks) << a.c.bs_log;
-    const long long pos = static_cast<long long>(__ldg(a.ctx_len + r)) + (t - first);
-    const long long see = min(min(pos + 1, static_cast<long long>(__ldg(a.seq_len + r))), cap);
-    Row<D, CODE> row;
-    const long long qa = t * a.q_token_stride + h * a.q_head_stride + lane * E;
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      row.q[i] = a.fp16 ? __half2float(static_cast<const __half*>(a.q)[qa + i])
-                        : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[qa + i]);
-    row.start();
-    bool bad = false;
-    for (long long j = 0; j < see; ++j) {
-      const int block = __ldg(a.table + (long long)r * a.max_blocks + (j >> a.c.bs_log));
-      if (block < 0 || block >= a.c.blocks) { bad = true; continue; }
-      row.key(a.c, block, h / a.group, static_cast<int>(j & (a.c.bs - 1)), lane, a.scale_log2);
-    }
-    if (bad && lane == 0) cache_flag(a.dev_err, ALHR_DEVERR_BLOCK);
-    const float inv = row.l > 0.f ? 1.f / row.l : 0.f;
-#pragma unroll
-    for (int i = 0; i < E; i += 2)
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + u * D + lane * E + i) =
-          pack2(row.o[i] * inv, row.o[i + 1] * inv, a.fp16);
-    if (a.lse && lane == 0)
-      a.lse[u] = row.l > 0.f ? (row.m + log2f(row.l)) * 0.6931471805599453f : -INFINITY;
-  }
-}
-
-template <int D, int CODE>
 __global__ void __launch_bounds__(kRowWarps * 32) attend_selected_kernel(const SelectArgs a) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
@@ -134,16 +91,10 @@ unsigned grid_of(long long rows) {
 
 }  // namespace
 
-size_t attend_cache_workspace(int, int) { return 16; }
+size_t attend_cache_workspace(int sms, int d) { return decode_workspace(sms, d); }
 
-cudaError_t launch_attend_cache(const AttendArgs& a, int d, int code, int, cudaStream_t st) {
-  const unsigned grid = grid_of(static_cast<long long>(a.tokens) * a.q_heads);
-  auto kernel = d == 64 ? (code == ALHR_CODE_INT8 ? attend_rows_kernel<64, ALHR_CODE_INT8>
-                                                  : attend_rows_kernel<64, ALHR_CODE_E4M3>)
-                        : (code == ALHR_CODE_INT8 ? attend_rows_kernel<128, ALHR_CODE_INT8>
-                                                  : attend_rows_kernel<128, ALHR_CODE_E4M3>);
-  kernel<<<grid, kRowWarps * 32, 0, st>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_attend_cache(const AttendArgs& a, int d, int code, int sms, cudaStream_t st) {
+  return launch_decode(a, d, code, sms, 0x7fffffff, st);
 }
 
 cudaError_t launch_attend_selected(const SelectArgs& a, int d, int code, int, cudaStream_t st) {

@@ -1,0 +1,638 @@
+// cache_decode.cu -- attention of few query rows a request over all of its keys (decode).
+//
+// Mathematics: with x_j = s_j log2 e + log2 v_scale_j (s_j the scaled score) and M near the running
+// maximum of x, the weights w_j = 2^(x_j - M) multiply the value codes, O = sum w_j vcode_j, and
+// l = sum w_j / v_scale_j is the softmax's sum: out = O / l. Taking the block's value scale into
+// the exponent keeps the weights of blocks with very different scales in the range of a half: M is
+// chosen so that the largest weight lies in [2^7, 2^15], and weights down to 2^-21 of it are
+// rounded at 2^-11 of themselves. l is summed from the fp32 weights.
+//
+// What bounds it: the codes have to be read once, 2 d bytes a key and head; everything else is
+// there to keep the memory busy. The tiles of all (request, key head, row group) units form one
+// list, and each warp of the GPU takes an equal, contiguous piece of it: no unit is too short or
+// too long, and no warp waits for another one. A warp copies its tiles (32 keys at d = 128, 64 at
+// d = 64: 8 KB) kStages ahead into its own piece of shared memory, converts the codes to halves
+// in registers and uses the warp-wide matrix product. A unit inside one warp's piece is written at
+// once; one that spans pieces leaves partial sums (O, M, l), which a second kernel joins in the
+// order of the pieces.
+#include <cmath>
+
+#include "cache_mma.cuh"
+
+namespace alhr {
+
+namespace {
+
+constexpr int kDecodeWarps = 8;  // of one CTA a multiprocessor
+constexpr int kStages = 3;
+constexpr float kTopLog = 7.f;    // log2 of the largest weight when M is set
+constexpr int kStageBytes = 8192;  // codes of one tile, keys and values
+
+template <int D>
+struct Tile {
+  static constexpr int kKeys = kStageBytes / (2 * D);
+  static constexpr int kSubs = kKeys / 16;         // groups of 16 keys: one block each
+  static constexpr int kScaleBytes = kSubs * 16;   // {k scale, v scale, there} of each group
+  static constexpr int kStride = kStageBytes + 64;
+  static_assert(kScaleBytes <= 64, "scales behind the codes");
+};
+
+// Key of the tile's 16-key group that row m (0..7, and m + 8 likewise) of the product stands for.
+// At d = 64 two rows share 128 bytes; this order keeps both reads below free of bank conflicts.
+template <int D>
+__device__ __forceinline__ int key_of(int m) {
+  return D == 128 ? m : (m & 4) | ((0x2130 >> (4 * (m & 3))) & 3);  // 0 3 1 2 4 7 5 6
+}
+
+// 16-byte piece c of row `row`, where it lies in shared memory.
+template <int D>
+__device__ __forceinline__ int piece_offset(int row, int c) {
+  return D == 128 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+}
+
+struct Partial {
+  int unit_r, unit_h, unit_rows0, rows;  // of the unit that starts here and ends elsewhere
+  int last;                              // the piece that ends it; -1: none
+};
+
+// Which pieces of the tile list there are.
+struct Split {
+  long long tiles;
+  int pieces;
+  __device__ __forceinline__ long long first(int i) const { return tiles * i / pieces; }
+  __device__ __forceinline__ int piece_of(long long tile) const {
+    return static_cast<int>(((tile + 1) * pieces - 1) / tiles);
+  }
+};
+
+// One request as the list sees it.
+template <int D, int ROWS>
+struct Request {
+  int q_lo, rows, ctx, see, tiles, groups;
+  __device__ __forceinline__ void load(const AttendArgs& a, int r, int row_limit) {
+    q_lo = min(max(__ldg(a.q_start + r), 0), a.tokens);
+    const int q_hi = min(max(__ldg(a.q_start + r + 1), q_lo), a.tokens);
+    ctx = __ldg(a.ctx_len + r);
+    const long long cap = static_cast<long long>(a.max_blocks) << a.c.bs_log;
+    const long long end = min(min(static_cast<long long>(ctx) + (q_hi - q_lo),
+                                  static_cast<long long>(__ldg(a.seq_len + r))), cap);
+    see = static_cast<int>(max(end, 0LL));
+    rows = (q_hi - q_lo) * a.group;
+    groups = rows > row_limit ? 0 : (rows + ROWS - 1) / ROWS;
+    tiles = max(1, (see + Tile<D>::kKeys - 1) / Tile<D>::kKeys);
+  }
+  __device__ __forceinline__ long long work(int heads) const {
+    return static_cast<long long>(groups) * tiles * heads;
+  }
+};
+
+template <int D, int ROWS>
+struct Cursor {
+  Request<D, ROWS> q;
+  int r, h, group, tile;
+  __device__ __forceinline__ void step(const AttendArgs& a, int row_limit) {
+    if (++tile < q.tiles) return;
+    tile = 0;
+    if (++group < q.groups) return;
+    group = 0;
+    if (++h < a.c.heads) return;
+    h = 0;
+    do {
+      if (++r >= a.requests) {  // not reached: the list has ended before
+        r = a.requests - 1;
+        return;
+      }
+      q.load(a, r, row_limit);
+    } while (q.groups == 0);
+  }
+};
+
+// Floats of one partial: O [ROWS][D], M [ROWS], l [ROWS].
+template <int D, int ROWS>
+constexpr int partial_floats() { return ROWS * (D + 2); }
+
+struct DecodeSpace {
+  Partial* meta;  // [pieces]
+  float* part;    // [pieces][2][partial_floats]: a unit begun earlier, a unit begun here
+};
+
+__device__ __forceinline__ float group_max(float v) {  // over the lanes of equal lane % 4
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float group_add(float v) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <int D, int CODE, int NT>
+__global__ void __launch_bounds__(kDecodeWarps * 32, 1)
+    decode_kernel(const AttendArgs a, const DecodeSpace space, const int row_limit) {
+  constexpr int ROWS = 8 * NT;
+  constexpr int KS = D / 16;              // products over d of one 16-key group
+  constexpr int SUBS = Tile<D>::kSubs;
+  constexpr int LPR = D / 16;             // 16-byte pieces of a row
+  constexpr int RPI = 32 / LPR;           // rows one copy of the warp covers
+  extern __shared__ __align__(128) unsigned char decode_smem[];
+  __shared__ long long chunk_start[kDecodeWarps * 32 + 1];
+  __shared__ long long warp_sum[kDecodeWarps];
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+
+  // ---- the tile list: every thread sums a run of requests
+  const int per = (a.requests + kDecodeWarps * 32 - 1) / (kDecodeWarps * 32);
+  Cursor<D, ROWS> load;
+  long long sum = 0;
+  for (int r = tid * per; r < min(a.requests, (tid + 1) * per); ++r) {
+    load.q.load(a, r, row_limit);
+    sum += load.q.work(a.c.heads);
+  }
+  long long incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kDecodeWarps; ++w) {
+    before += w < warp ? warp_sum[w] : 0;
+    all += warp_sum[w];
+  }
+  chunk_start[tid] = before + incl - sum;
+  if (tid == 0) chunk_start[kDecodeWarps * 32] = all;
+  __syncthreads();
+
+  // a short list is cut into single tiles, so that every piece it has holds one at least
+  const long long most = static_cast<long long>(gridDim.x) * kDecodeWarps;
+  const Split split{all, static_cast<int>(min(most, all))};
+  // pieces beside one another in the list lie on different multiprocessors
+  const int piece = warp * gridDim.x + blockIdx.x;
+  const long long begin = piece < split.pieces ? split.first(piece) : 0;
+  const long long end = piece < split.pieces ? split.first(piece + 1) : 0;
+  Partial* meta = space.meta + piece;
+  if (lane == 0) meta->last = -1;
+  if (begin >= end) return;
+
+  // ---- where this piece begins
+  {
+    int lo = 0, hi = kDecodeWarps * 32 - 1;  // the last chunk that starts at or before `begin`
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (chunk_start[mid] <= begin) lo = mid;
+      else hi = mid - 1;
+    }
+    // chunks without work share their start with the next one: the last of them has the work
+    long long at = chunk_start[lo];
+    load.r = lo * per;
+    for (;;) {
+      load.q.load(a, load.r, row_limit);
+      const long long w = load.q.work(a.c.heads);
+      if (begin < at + w) break;
+      at += w;
+      if (++load.r >= a.requests) return;  // not reached: `begin` is inside the list
+    }
+    long long rest = begin - at;
+    const long long per_head = static_cast<long long>(load.q.groups) * load.q.tiles;
+    load.h = static_cast<int>(rest / per_head);
+    rest -= load.h * per_head;
+    load.group = static_cast<int>(rest / load.q.tiles);
+    load.tile = static_cast<int>(rest - static_cast<long long>(load.group) * load.q.tiles);
+  }
+  Cursor<D, ROWS> cur = load;
+
+  // ---- copies, kStages tiles ahead
+  const uint32_t ring = shared_u32(decode_smem) + warp * (kStages * Tile<D>::kStride);
+  const int crow = lane / LPR, cpiece = lane % LPR;
+  bool bad = false;
+  // block of 16-key group `lane` of the loader's tile; -1: no visible key in it; -2: a bad number
+  auto fetch_block = [&]() {
+    int block = -1;
+    const int key = load.tile * Tile<D>::kKeys + lane * 16;
+    if (lane < SUBS && key < load.q.see) {
+      block = __ldg(a.table + static_cast<long long>(load.r) * a.max_blocks + (key >> a.c.bs_log));
+      if (block < 0 || block >= a.c.blocks) block = -2;
+    }
+    return block;
+  };
+  int next_block = fetch_block();
+  auto issue = [&](int stage) {
+    const uint32_t base = ring + stage * Tile<D>::kStride;
+    bad |= next_block == -2;
+#pragma unroll
+    for (int s = 0; s < SUBS; ++s) {
+      const int block = __shfl_sync(0xffffffffu, next_block, s);
+      const int key0 = load.tile * Tile<D>::kKeys + s * 16;
+      const int there = block >= 0 ? min(16, load.q.see - key0) : 0;  // rows of the group to copy
+      const long long row0 =
+          block_row(a.c, max(block, 0), load.h) + (key0 & (a.c.bs - 1));
+#pragma unroll
+      for (int i = 0; i < 16 / RPI; ++i) {
+        const int row = i * RPI + crow;  // of the group
+        const int n = row < there ? 16 : 0;
+        const long long src = (row0 + (n ? row : 0)) * D + (n ? cpiece * 16 : 0);
+        const uint32_t dst = base + s * 16 * D + piece_offset<D>(row, cpiece);
+        copy16(dst, a.c.k + src, n);
+        copy16(dst + kStageBytes / 2, a.c.v + src, n);
+      }
+    }
+    if (lane < SUBS) {
+      const long long si =
+          static_cast<long long>(max(next_block, 0)) * a.c.heads + load.h;
+      const uint32_t dst = base + kStageBytes + lane * 16;
+      const int n = next_block >= 0 ? 4 : 0;
+      copy4(dst, a.c.k_scale + si, n);
+      copy4(dst + 4, a.c.v_scale + si, n);
+      asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(dst + 8), "r"(next_block >= 0 ? 1 : 0) : "memory");
+    }
+  };
+  long long loaded = begin;
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) {
+    if (loaded < end) {
+      issue(s);
+      if (++loaded < end) {
+        load.step(a, row_limit);
+        next_block = fetch_block();
+      }
+    }
+    copy_commit();
+  }
+
+  // ---- the unit's queries
+  uint32_t qf[NT][KS][2];
+  float qscale[NT][2];  // factor of the scores of columns 2 t, 2 t + 1
+  int see[NT][2];       // visible keys of those columns' rows
+  float o[NT][KS][4], m[NT][2], l[NT][2];
+  int see_min;
+  auto begin_unit = [&]() {
+    const int row0 = cur.group * ROWS;
+    see_min = 0x7fffffff;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = row0 + n * 8 + g;
+      float x[D / 4];
+      float top = 0.f;
+      if (row < cur.q.rows) {
+        const int tok = row / a.group;
+        const long long at = (cur.q.q_lo + tok) * a.q_token_stride +
+                             (cur.h * a.group + (row - tok * a.group)) * a.q_head_stride + t * (D / 4);
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const uint4 w = __ldg(p + i);
+          float y[8];
+          if (a.fp16) unpack8<ALHR_TYPE_FP16>(w, w, y);
+          else unpack8<ALHR_TYPE_BF16>(w, w, y);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            x[8 * i + j] = y[j];
+            top = fmaxf(top, fabsf(y[j]));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) x[i] = 0.f;
+      }
+      // a row is scaled by the power of two that brings its largest number to [2^14, 2^15), so
+      // that its halves are exact down to 2^-28 of it
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100), 126);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        qf[n][s][0] = pack2(x[4 * s] * up, x[4 * s + 1] * up, true);
+        qf[n][s][1] = pack2(x[4 * s + 2] * up, x[4 * s + 3] * up, true);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        qscale[n][c] = __shfl_sync(0xffffffffu, down, 4 * (2 * t + c)) * a.scale_log2;
+        const int cr = row0 + n * 8 + 2 * t + c;
+        const long long pos = static_cast<long long>(cur.q.ctx) + cr / a.group + 1;
+        see[n][c] = cr < cur.q.rows
+                        ? static_cast<int>(max(min(pos, static_cast<long long>(cur.q.see)), 0LL)) : 0;
+        if (cr < cur.q.rows) see_min = min(see_min, see[n][c]);
+        m[n][c] = -INFINITY;
+        l[n][c] = 0.f;
+      }
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[n][s][i] = 0.f;
+    }
+    see_min = __reduce_min_sync(0xffffffffu, see_min);
+  };
+
+  // column c of column group n: row, sums over the keys of all lanes
+  auto end_unit = [&](bool from_start, bool to_end) {
+    const int row0 = cur.group * ROWS;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float sum_l = group_add(l[n][c]);
+        const int col = n * 8 + 2 * t + c, row = row0 + col;
+        if (row >= cur.q.rows) continue;
+        float y[D / 8];  // numbers [g * D / 8, (g + 1) * D / 8) of the row
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          y[2 * s] = o[n][s][c];
+          y[2 * s + 1] = o[n][s][2 + c];
+        }
+        if (from_start && to_end) {
+          const float inv = sum_l > 0.f ? 1.f / sum_l : 0.f;
+          const int tok = row / a.group;
+          const long long at = static_cast<long long>(cur.q.q_lo + tok) * a.q_heads +
+                               cur.h * a.group + (row - tok * a.group);
+          uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D + g * (D / 8));
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i)
+            p[i] = make_uint4(pack2(y[8 * i] * inv, y[8 * i + 1] * inv, a.fp16),
+                              pack2(y[8 * i + 2] * inv, y[8 * i + 3] * inv, a.fp16),
+                              pack2(y[8 * i + 4] * inv, y[8 * i + 5] * inv, a.fp16),
+                              pack2(y[8 * i + 6] * inv, y[8 * i + 7] * inv, a.fp16));
+          if (a.lse && g == 0)
+            a.lse[at] = sum_l > 0.f ? (m[n][c] + log2f(sum_l)) * 0.6931471805599453f : -INFINITY;
+        } else {
+          float* part = space.part + (static_cast<long long>(piece) * 2 + (from_start ? 1 : 0)) *
+                                         partial_floats<D, ROWS>();
+          float4* p = reinterpret_cast<float4*>(part + col * D + g * (D / 8));
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)
+            p[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          if (g == 0) {
+            part[ROWS * D + col] = m[n][c];
+            part[ROWS * D + ROWS + col] = sum_l;
+          }
+        }
+      }
+    }
+    if (from_start && !to_end && lane == 0) {
+      meta->unit_r = cur.r;
+      meta->unit_h = cur.h;
+      meta->unit_rows0 = row0;
+      meta->rows = min(ROWS, cur.q.rows - row0);
+      // the unit's last tile: this piece ends inside the unit, at list position `end`
+      meta->last = split.piece_of(end - 1 + (cur.q.tiles - 1 - cur.tile));
+    }
+  };
+
+  begin_unit();
+  bool from_start = cur.tile == 0;
+  int stage = 0;
+  for (long long f = begin; f < end; ++f) {
+    copy_wait<kStages - 1>();
+    __syncwarp();
+    const uint32_t base = ring + stage * Tile<D>::kStride;
+    // scores
+    float s[SUBS][NT][4];
+    float add[SUBS], inv_vs[SUBS];
+#pragma unroll
+    for (int u = 0; u < SUBS; ++u) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[u][n][i] = 0.f;
+      const int r0 = u * 16 + key_of<D>(g);
+      uint32_t w0[D / 16], w1[D / 16];  // D / 4 codes of rows g and g + 8
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const uint4 x = lds128(base + piece_offset<D>(r0, t * (D / 64) + i));
+        const uint4 y = lds128(base + piece_offset<D>(r0 + 8, t * (D / 64) + i));
+        w0[4 * i] = x.x; w0[4 * i + 1] = x.y; w0[4 * i + 2] = x.z; w0[4 * i + 3] = x.w;
+        w1[4 * i] = y.x; w1[4 * i + 1] = y.y; w1[4 * i + 2] = y.z; w1[4 * i + 3] = y.w;
+      }
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t a0, a1, a2, a3;
+        widen4<CODE>(w0[k], a0, a2);
+        widen4<CODE>(w1[k], a1, a3);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma16816(s[u][n], a0, a1, a2, a3, qf[n][k][0], qf[n][k][1]);
+      }
+      const uint4 sc = lds128(base + kStageBytes + u * 16);
+      const float vs = fmaxf(__uint_as_float(sc.y), kTinyScale);
+      add[u] = sc.z ? __log2f(vs) : -INFINITY;
+      inv_vs[u] = sc.z ? __frcp_rn(vs) : 0.f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float f1 = qscale[n][c] * __uint_as_float(sc.x);
+          s[u][n][c] = fmaf(s[u][n][c], f1, add[u]);
+          s[u][n][2 + c] = fmaf(s[u][n][2 + c], f1, add[u]);
+        }
+    }
+    const int key0 = cur.tile * Tile<D>::kKeys;
+    if (key0 + Tile<D>::kKeys > see_min) {  // some row does not see the whole tile
+#pragma unroll
+      for (int u = 0; u < SUBS; ++u) {
+        const int k0 = key0 + u * 16 + key_of<D>(g);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (k0 + (i >> 1) * 8 >= see[n][i & 1]) s[u][n][i] = -INFINITY;
+      }
+    }
+    // M moves only when it has to: the largest weight is between 2^7 and 2^15
+    bool grow = false;
+    float top[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float x = fmaxf(s[0][n][c], s[0][n][2 + c]);
+#pragma unroll
+        for (int u = 1; u < SUBS; ++u) x = fmaxf(x, fmaxf(s[u][n][c], s[u][n][2 + c]));
+        top[n][c] = group_max(x);
+        grow |= top[n][c] > m[n][c] + kTopLog + 8.f;
+      }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float mn = fmaxf(m[n][c], top[n][c] - kTopLog);
+          const float keep = mn == -INFINITY ? 1.f : exp2_fast(m[n][c] - mn);
+          m[n][c] = mn;
+          l[n][c] *= keep;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            o[n][k][c] *= keep;
+            o[n][k][2 + c] *= keep;
+          }
+        }
+    }
+    // weights, as the second product's operand
+    uint32_t pf[SUBS][NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0];
+      const float m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+#pragma unroll
+      for (int u = 0; u < SUBS; ++u) {
+        const float p0 = exp2_fast(s[u][n][0] - m0), p1 = exp2_fast(s[u][n][1] - m1);
+        const float p2 = exp2_fast(s[u][n][2] - m0), p3 = exp2_fast(s[u][n][3] - m1);
+        l[n][0] = fmaf(p0 + p2, inv_vs[u], l[n][0]);
+        l[n][1] = fmaf(p1 + p3, inv_vs[u], l[n][1]);
+        pf[u][n][0] = transpose8x8(pack2(p0, p1, true));
+        pf[u][n][1] = transpose8x8(pack2(p2, p3, true));
+      }
+    }
+    // values: lane (g, t) takes numbers [g D / 8, (g + 1) D / 8) of four keys
+#pragma unroll
+    for (int u = 0; u < SUBS; ++u) {
+      constexpr int W = D / 32;  // words of a row
+      uint32_t v[4][W];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = u * 16 + key_of<D>(2 * t + (i & 1)) + (i >> 1) * 8;
+        if constexpr (D == 128) {
+          const uint4 x = lds128(base + kStageBytes / 2 + piece_offset<D>(row, g));
+          v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
+        } else {
+          const uint2 x = lds64(base + kStageBytes / 2 + piece_offset<D>(row, g >> 1) + (g & 1) * 8);
+          v[i][0] = x.x; v[i][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        // pairs of keys of the same number: {a, b} of numbers 4 w .. 4 w + 3
+        uint32_t x0, x1, x2, x3, y0, y1, y2, y3;
+        widen4<CODE>(prmt(v[0][w], v[1][w], 0x5140), x0, x1);
+        widen4<CODE>(prmt(v[0][w], v[1][w], 0x7362), x2, x3);
+        widen4<CODE>(prmt(v[2][w], v[3][w], 0x5140), y0, y1);
+        widen4<CODE>(prmt(v[2][w], v[3][w], 0x7362), y2, y3);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma16816(o[n][2 * w], x0, x1, y0, y1, pf[u][n][0], pf[u][n][1]);
+          mma16816(o[n][2 * w + 1], x2, x3, y2, y3, pf[u][n][0], pf[u][n][1]);
+        }
+      }
+    }
+    __syncwarp();  // every lane has read the stage
+    if (loaded < end) {
+      issue(stage);
+      if (++loaded < end) {
+        load.step(a, row_limit);
+        next_block = fetch_block();
+      }
+    }
+    copy_commit();
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    const bool to_end = cur.tile + 1 == cur.q.tiles;
+    if (to_end || f + 1 == end) {
+      end_unit(from_start, to_end);
+      from_start = true;
+      if (f + 1 < end) {
+        cur.step(a, row_limit);
+        begin_unit();
+      }
+    } else {
+      ++cur.tile;
+    }
+  }
+  copy_wait<0>();
+  if (__any_sync(0xffffffffu, bad) && lane == 0) cache_flag(a.dev_err, ALHR_DEVERR_BLOCK);
+}
+
+// Joins the partial sums of the units that span pieces: one CTA for each piece in which such a
+// unit begins, one warp a row.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(ROWS * 32) decode_join_kernel(const AttendArgs a,
+                                                                const DecodeSpace space) {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const int piece = blockIdx.x, lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+  const Partial p = space.meta[piece];
+  if (p.last < 0 || row >= p.rows) return;
+  constexpr int E = D / 32;
+  constexpr int kStep = partial_floats<D, ROWS>();
+  // partials: slot 1 of this piece, slot 0 of the pieces behind it
+  const int n = p.last - piece + 1;
+  auto part = [&](int i) {
+    return space.part + (static_cast<long long>(piece + i) * 2 + (i == 0 ? 1 : 0)) * kStep;
+  };
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, part(i)[ROWS * D + row]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float base = m == -INFINITY ? 0.f : m;
+  float acc[E], l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float* x = part(i);
+    const float f = exp2_fast(x[ROWS * D + row] - base);
+    l = fmaf(x[ROWS * D + ROWS + row], f, l);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(x[row * D + lane * E + e], f, acc[e]);
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int rr = p.unit_rows0 + row, tok = rr / a.group;
+  const int q_lo = min(max(__ldg(a.q_start + p.unit_r), 0), a.tokens);
+  const long long at = static_cast<long long>(q_lo + tok) * a.q_heads + p.unit_h * a.group +
+                       (rr - tok * a.group);
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at * D + lane * E + e) =
+        pack2(acc[e] * inv, acc[e + 1] * inv, a.fp16);
+  if (a.lse && lane == 0) a.lse[at] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <int D, int CODE, int NT>
+cudaError_t decode_as(const AttendArgs& a, int sms, int row_limit, cudaStream_t st) {
+  static thread_local bool configured[128] = {};
+  constexpr int kSmem = kDecodeWarps * kStages * Tile<D>::kStride;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 128 || !configured[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        decode_kernel<D, CODE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 128) configured[dev] = true;
+  }
+  const int pieces = sms * kDecodeWarps;
+  DecodeSpace space;
+  space.meta = static_cast<Partial*>(a.workspace);
+  space.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + pieces * 32);
+  decode_kernel<D, CODE, NT><<<sms, kDecodeWarps * 32, kSmem, st>>>(a, space, row_limit);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  decode_join_kernel<D, 8 * NT><<<pieces, 8 * NT * 32, 0, st>>>(a, space);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t decode_workspace(int sms, int d) {
+  return static_cast<size_t>(sms) * kDecodeWarps * (32 + 2 * 16 * (d + 2) * sizeof(float));
+}
+
+// Requests of at most row_limit rows (of one key head).
+cudaError_t launch_decode(const AttendArgs& a, int d, int code, int sms, int row_limit,
+                          cudaStream_t st) {
+  const long long rows = static_cast<long long>(a.max_q < a.tokens ? a.max_q : a.tokens) * a.group;
+  const bool one = rows <= 8;
+  if (d == 64)
+    return code == ALHR_CODE_INT8
+               ? (one ? decode_as<64, ALHR_CODE_INT8, 1>(a, sms, row_limit, st)
+                      : decode_as<64, ALHR_CODE_INT8, 2>(a, sms, row_limit, st))
+               : (one ? decode_as<64, ALHR_CODE_E4M3, 1>(a, sms, row_limit, st)
+                      : decode_as<64, ALHR_CODE_E4M3, 2>(a, sms, row_limit, st));
+  return code == ALHR_CODE_INT8
+             ? (one ? decode_as<128, ALHR_CODE_INT8, 1>(a, sms, row_limit, st)
+                    : decode_as<128, ALHR_CODE_INT8, 2>(a, sms, row_limit, st))
+             : (one ? decode_as<128, ALHR_CODE_E4M3, 1>(a, sms, row_limit, st)
+                    : decode_as<128, ALHR_CODE_E4M3, 2>(a, sms, row_limit, st));
+}
+
+}  // namespace alhr
