@@ -51,23 +51,21 @@ class SelectionStruct(ctypes.Structure):
                 [("scale", ctypes.c_float)])
 
 
+# The checks below run before every launch of a few microseconds: they read each attribute once.
+
 def _need(t, dtype, shape, name, device):
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)}, got "
-                         f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.device != device:
         raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)}, got "
+                     f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}")
 
 
 def _cuda(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor")
     return t.device
-
-
-def _int32(t, shape, name, device):
-    _need(t, torch.int32, shape, name, device)
-    return t.data_ptr()
 
 
 def _err(dev_err, device):
@@ -79,14 +77,19 @@ def _err(dev_err, device):
     return dev_err.data_ptr()
 
 
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream  # the handle itself, without an object
+
+
 def _call(name, device, *args):
     """The entry point on `device` and its current stream."""
     fn = getattr(alhr.lib(), name)
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    index = device.index
+    if _current_device() == index:
+        status = fn(*args, _current_stream(index))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream().cuda_stream)
+            status = fn(*args, _current_stream(index))
     if status != alhr.ALHR_OK:
         raise alhr.AlhrError(status, name)
 
@@ -98,12 +101,12 @@ def _struct(cache, device):
         raise ValueError(f"cache k: expected int8 or float8_e4m3fn [blocks, heads, block_size, d],"
                          f" got {k.dtype} {tuple(k.shape)}")
     blocks, heads, bs, d = k.shape
-    _need(k, k.dtype, k.shape, "cache k", device)
-    _need(v, k.dtype, k.shape, "cache v", device)
-    _need(ks, torch.float32, (blocks, heads), "cache k_scale", device)
-    _need(vs, torch.float32, (blocks, heads), "cache v_scale", device)
-    return CacheStruct(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), blocks, heads, bs,
-                       d, _CODES[k.dtype])
+    scales = (blocks, heads)
+    return CacheStruct(_need(k, k.dtype, k.shape, "cache k", device),
+                       _need(v, k.dtype, k.shape, "cache v", device),
+                       _need(ks, torch.float32, scales, "cache k_scale", device),
+                       _need(vs, torch.float32, scales, "cache v_scale", device),
+                       blocks, heads, bs, d, _CODES[k.dtype])
 
 
 def alloc_cache(blocks: int, heads: int, block_size: int, d: int, dtype=torch.int8,
@@ -138,16 +141,16 @@ def plan_blocks(ctx_len: torch.Tensor, new_len: torch.Tensor, block_table: torch
     tokens = int(tokens)
     if tokens < 0:
         raise ValueError(f"tokens {tokens}: at least 0")
-    ctx = _int32(ctx_len, (r,), "ctx_len", dev)
-    new = _int32(new_len, (r,), "new_len", dev)
-    table = _int32(block_table, (r, width), "block_table", dev)
-    free = _int32(free_blocks, free_blocks.shape, "free_blocks", dev)
-    first = _int32(free_first, (1,), "free_first", dev)
-    q_start = torch.empty(r + 1, dtype=torch.int32, device=dev)
-    seq_len = torch.empty(r, dtype=torch.int32, device=dev)
-    slots = torch.empty(tokens, dtype=torch.int64, device=dev)
-    positions = torch.empty(tokens, dtype=torch.int32, device=dev)
-    free_next = torch.empty(1, dtype=torch.int32, device=dev)
+    ctx = _need(ctx_len, torch.int32, (r,), "ctx_len", dev)
+    new = _need(new_len, torch.int32, (r,), "new_len", dev)
+    table = _need(block_table, torch.int32, (r, width), "block_table", dev)
+    free = _need(free_blocks, torch.int32, free_blocks.shape, "free_blocks", dev)
+    first = _need(free_first, torch.int32, (1,), "free_first", dev)
+    q_start = ctx_len.new_empty(r + 1)
+    seq_len = ctx_len.new_empty(r)
+    slots = ctx_len.new_empty(tokens, dtype=torch.int64)
+    positions = ctx_len.new_empty(tokens)
+    free_next = ctx_len.new_empty(1)
     _call("alhr_plan_blocks", dev, r, width, block_size, min(blocks, (2**31 - 1) // block_size),
           tokens, free_blocks.numel(), ctx, new, table, free, first, q_start.data_ptr(),
           seq_len.data_ptr(), slots.data_ptr(), positions.data_ptr(), free_next.data_ptr(),
@@ -199,8 +202,8 @@ def load_cache(cache: dict, slots: torch.Tensor, dtype=torch.bfloat16,
         raise ValueError(f"slots: expected [tokens], got {tuple(slots.shape)}")
     t = slots.shape[0]
     _need(slots, torch.int64, (t,), "slots", dev)
-    K = torch.empty((t, c.heads, c.d), dtype=dtype, device=dev)
-    V = torch.empty((t, c.heads, c.d), dtype=dtype, device=dev)
+    K = slots.new_empty((t, c.heads, c.d), dtype=dtype)
+    V = slots.new_empty((t, c.heads, c.d), dtype=dtype)
     _call("alhr_load_cache", dev, ctypes.byref(c), K.data_ptr(), V.data_ptr(), _TYPES[dtype], t,
           slots.data_ptr(), _err(dev_err, dev))
     return dict(K=K, V=V)
@@ -231,22 +234,22 @@ def attend_cache(Q: torch.Tensor, cache: dict, block_table: torch.Tensor, ctx_le
     t, hq, _ = Q.shape
     r, width = block_table.shape
     qt, qh = _rows(Q, (t, hq, c.d), Q.dtype, "Q", dev)
-    table = _int32(block_table, (r, width), "block_table", dev)
-    ctx = _int32(ctx_len, (r,), "ctx_len", dev)
-    seq = _int32(seq_len, (r,), "seq_len", dev)
-    start = _int32(q_start, (r + 1,), "q_start", dev)
+    table = _need(block_table, torch.int32, (r, width), "block_table", dev)
+    ctx = _need(ctx_len, torch.int32, (r,), "ctx_len", dev)
+    seq = _need(seq_len, torch.int32, (r,), "seq_len", dev)
+    start = _need(q_start, torch.int32, (r + 1,), "q_start", dev)
     if max_q is not None and max_q < 1 and t > 0:
         raise ValueError(f"max_q {max_q}: at least 1, or None")
     if out is None:
-        out = torch.empty((t, hq, c.d), dtype=Q.dtype, device=dev)
+        out = Q.new_empty((t, hq, c.d))
     else:
         _need(out, Q.dtype, (t, hq, c.d), "out", dev)
-    lse = torch.empty((t, hq), dtype=torch.float32, device=dev) if want_lse else None
+    lse = Q.new_empty((t, hq), dtype=torch.float32) if want_lse else None
     q = QueriesStruct(r, t, hq, width, max_q or 0, _TYPES[Q.dtype], qt, qh,
                       1.0 / math.sqrt(c.d) if scale is None else scale)
     cp, qp = ctypes.byref(c), ctypes.byref(q)
     if workspace is None:
-        workspace = torch.empty(_workspace(cp, qp, dev), dtype=torch.uint8, device=dev)
+        workspace = Q.new_empty(_workspace(cp, qp, dev), dtype=torch.uint8)
     elif workspace.dtype != torch.uint8 or workspace.device != dev \
             or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected contiguous uint8 on {dev}")
@@ -257,7 +260,7 @@ def attend_cache(Q: torch.Tensor, cache: dict, block_table: torch.Tensor, ctx_le
 
 
 def _workspace(cp, qp, dev) -> int:
-    if torch.cuda.current_device() == dev.index:
+    if _current_device() == dev.index:
         return max(16, alhr.lib().alhr_attend_cache_workspace(cp, qp))
     with torch.cuda.device(dev):
         return max(16, alhr.lib().alhr_attend_cache_workspace(cp, qp))
@@ -292,11 +295,11 @@ def attend_cache_selected(Q: torch.Tensor, cache: dict, block_table: torch.Tenso
     B, H, nq, _ = Q.shape
     _need(Q, Q.dtype, (B, H, nq, c.d), "Q", dev)
     width, keys = block_table.shape[1], idx.shape[3]
-    table = _int32(block_table, (B, width), "block_table", dev)
-    ctx = _int32(ctx_len, (B,), "ctx_len", dev)
-    seq = _int32(seq_len, (B,), "seq_len", dev)
-    ip = _int32(idx, (B, H, nq, keys), "idx", dev)
-    np_ = _int32(count, (B, H, nq), "count", dev)
+    table = _need(block_table, torch.int32, (B, width), "block_table", dev)
+    ctx = _need(ctx_len, torch.int32, (B,), "ctx_len", dev)
+    seq = _need(seq_len, torch.int32, (B,), "seq_len", dev)
+    ip = _need(idx, torch.int32, (B, H, nq, keys), "idx", dev)
+    np_ = _need(count, torch.int32, (B, H, nq), "count", dev)
     if out is None:
         out = torch.empty((B, H, nq, c.d), dtype=torch.float32, device=dev)
     else:
