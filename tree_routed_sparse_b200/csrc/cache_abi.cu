@@ -171,10 +171,15 @@ alhr_status alhr_load_cache(const alhr_cache* cache, void* K, void* V, int32_t t
                                            static_cast<cudaStream_t>(stream)));
 }
 
+static size_t workspace_of(const alhr_cache* c, const alhr_cache_queries* q, int sms) {
+  const int64_t most = q->max_q == 0 || q->max_q > q->tokens ? q->tokens : q->max_q;
+  return alhr::attend_cache_workspace(sms, c->d, most * (q->q_heads / c->heads));
+}
+
 size_t alhr_attend_cache_workspace(const alhr_cache* cache, const alhr_cache_queries* queries) {
   if (check_queries(cache, queries) != ALHR_OK) return 0;
   const int sms = multiprocessors();
-  return sms ? alhr::attend_cache_workspace(sms, cache->d) : 0;
+  return sms ? workspace_of(cache, queries, sms) : 0;
 }
 
 alhr_status alhr_attend_cache(const alhr_cache* cache, const alhr_cache_queries* queries,
@@ -192,7 +197,7 @@ alhr_status alhr_attend_cache(const alhr_cache* cache, const alhr_cache_queries*
   if (!aligned16(Q) || !aligned16(out)) return ALHR_ERR_INVALID_ARG;
   const int sms = multiprocessors();
   if (!sms) return ALHR_ERR_CUDA;
-  if (workspace_bytes < alhr::attend_cache_workspace(sms, cache->d)) return ALHR_ERR_INVALID_ARG;
+  if (workspace_bytes < workspace_of(cache, queries, sms)) return ALHR_ERR_INVALID_ARG;
   alhr::AttendArgs a{};
   a.c = view_of(cache);
   a.q = Q; a.out = out; a.lse = lse;

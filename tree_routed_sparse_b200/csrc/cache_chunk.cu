@@ -1,0 +1,725 @@
+// cache_chunk.cu -- attention of many query rows a request over all of its keys (prompts, chunks).
+//
+// Mathematics as in cache_decode.cu: x_j = s_j log2 e + log2 v_scale_j, weights 2^(x_j - M) times
+// value codes, l = sum w_j / v_scale_j.
+//
+// What bounds it: the two products, 4 d flops a row and key, and one power of two a row and key;
+// at d = 128 the tensor core and the special-function unit need the same time. One CTA a
+// multiprocessor takes 256 query rows (two tiles of 128) of one key head and walks key tiles of
+// 128. Four warps load codes to registers, widen them to halves (exact) and write them to shared
+// memory in the core-matrix layout of tcgen05 (8 rows of 16 bytes): for the keys (rows of the
+// second operand) K-major, and the same bytes read MN-major are the values' operand, so nothing is
+// transposed. One thread issues the products: S_i = Q_i K^T into tensor memory, and O_i += P_i V
+// with P_i read from tensor memory, where the rows' threads put it in place of S_i. While the
+// tensor core works on one tile of rows the threads of the other one take their powers of two.
+// Rows of a request are (token, head of the group) pairs, so that grouped heads share every key
+// tile.
+//
+// As in cache_decode.cu the key tiles of all units form one list of which every CTA takes an
+// equal, contiguous piece; units that span pieces leave partial sums that a second kernel joins.
+//
+// Every wait is bounded; when one runs out (not expected) the CTA stops, sets ALHR_DEVERR_TIMEOUT,
+// waits (bounded) for its products in flight and frees its tensor memory.
+#include <cmath>
+
+#include "cache_mma.cuh"
+#include "cache_split.cuh"
+
+namespace alhr {
+
+namespace {
+
+constexpr int kRows = 256;       // query rows of a unit: two tiles of 128
+constexpr int kKeys = 128;       // keys of a tile
+constexpr int kChunkThreads = 512;  // warps 0-3, 4-7: rows; 8-11: keys and values; 12: products
+constexpr uint32_t kWaits = 1u << 24;
+constexpr float kTopLog = 7.f;   // log2 of the largest weight when M is set
+
+template <int D>
+struct ChunkSmem {
+  static constexpr int kTile = 128 * D * 2;      // 128 rows of halves
+  static constexpr int q = 0;                    // two tiles
+  static constexpr int k = 2 * kTile;            // two tiles
+  static constexpr int v = 4 * kTile;            // two tiles
+  static constexpr int scales = 6 * kTile;       // [2][8] of {k scale, log2 v scale, 1 / v scale}
+  static constexpr int bars = scales + 2 * 8 * 16;
+  static constexpr int misc = bars + 32 * 8;
+  static constexpr int bytes = misc + 64;
+};
+
+enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kScFree = 8, kSFull = 10, kPFull = 12,
+           kQFull = 14, kODone = 16, kDrain = 18, kBars = 19 };
+
+__device__ __forceinline__ void bar_init(uint32_t bar, int count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+// Waits for the completion of the phase of this parity; false when the wait runs out or another
+// role has given up.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
+  for (uint32_t i = 0; i < kWaits; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((i & 63u) == 63u && *stop) return false;
+  }
+  *stop = 1;
+  return false;
+}
+
+// The same for a whole warp: all of its lanes go on, or none.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
+  return __all_sync(0xffffffffu, bar_wait(bar, parity, stop));
+}
+
+// Shared-memory operand descriptor without swizzle: start address, leading and stride byte offset.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) |
+         static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
+         static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32 | static_cast<uint64_t>(1) << 46;
+}
+
+// Instruction descriptor of kind::f16: fp32 sums, halves, M = 128, N columns; bit 16: the second
+// operand is MN-major.
+constexpr uint32_t product_desc(int n, bool mn_major) {
+  return (1u << 4) | (mn_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+
+__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void commit_to(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void fence_shared() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_ld32(uint32_t (&v)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+        "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
+        "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
+      "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+      "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};\n" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// One request of the list: more than row_limit rows; groups of kRows rows, each with the key tiles
+// that its last row sees.
+struct ChunkRequest {
+  int q_lo, rows, ctx, see, groups;
+  __device__ __forceinline__ void load(const AttendArgs& a, int r, int row_limit) {
+    const RequestRange q(a, r);
+    q_lo = q.q_lo;
+    ctx = q.ctx;
+    see = q.see;
+    rows = q.tokens * a.group;
+    groups = rows > row_limit ? (rows + kRows - 1) / kRows : 0;
+  }
+  __device__ __forceinline__ int tiles(const AttendArgs& a, int group) const {
+    const int last = min((group + 1) * kRows, rows) - 1;
+    const long long end = min(static_cast<long long>(ctx) + last / a.group + 1,
+                              static_cast<long long>(see));
+    return max(1, static_cast<int>((end + kKeys - 1) / kKeys));
+  }
+  __device__ __forceinline__ long long per_head(const AttendArgs& a) const {
+    long long n = 0;
+    for (int g = 0; g < groups; ++g) n += tiles(a, g);
+    return n;
+  }
+};
+
+struct ChunkCursor {
+  ChunkRequest q;
+  int r, h, group, tile, tiles;
+  // false when the next tile belongs to another unit
+  __device__ __forceinline__ void step(const AttendArgs& a, int row_limit) {
+    if (++tile < tiles) return;
+    tile = 0;
+    if (++group == q.groups) {
+      group = 0;
+      if (++h == a.c.heads) {
+        h = 0;
+        do {
+          if (++r >= a.requests) {  // not reached: the list has ended before
+            r = a.requests - 1;
+            q.groups = 1;
+            break;
+          }
+          q.load(a, r, row_limit);
+        } while (q.groups == 0);
+      }
+    }
+    tiles = q.tiles(a, group);
+  }
+  __device__ __forceinline__ int rows_here() const { return min(kRows, q.rows - group * kRows); }
+};
+
+template <int D, int CODE>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    chunk_kernel(const AttendArgs a, const JoinSpace space, const int row_limit) {
+  using L = ChunkSmem<D>;
+  constexpr int kCols = D / 8;  // 16-byte columns of a row of halves
+  extern __shared__ __align__(1024) unsigned char chunk_smem[];
+  __shared__ long long chunk_start[kChunkThreads];
+  __shared__ long long warp_sum[kChunkThreads / 32];
+  const uint32_t smem = shared_u32(chunk_smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t bars = smem + L::bars;
+  auto bar = [&](int which, int i = 0) { return bars + (which + i) * 8; };
+  volatile int* stop = reinterpret_cast<volatile int*>(chunk_smem + L::misc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(chunk_smem + L::misc + 16);
+
+  // ---- the tile list
+  const int per = (a.requests + kChunkThreads - 1) / kChunkThreads;
+  ChunkCursor cur;
+  long long sum = 0;
+  for (int r = tid * per; r < min(a.requests, (tid + 1) * per); ++r) {
+    cur.q.load(a, r, row_limit);
+    sum += cur.q.per_head(a) * a.c.heads;
+  }
+  const Split split = make_split<kChunkThreads>(sum, chunk_start, warp_sum, gridDim.x);
+  const int piece = blockIdx.x;
+  const long long begin = piece < split.pieces ? split.first(piece) : 0;
+  const long long end = piece < split.pieces ? split.first(piece + 1) : 0;
+  JoinMeta* meta = space.meta + piece;
+  if (tid == 0) meta->last = -1;
+  if (begin >= end) return;
+  {
+    const int c = chunk_of<kChunkThreads>(chunk_start, begin);
+    long long at = chunk_start[c], head = 0;
+    cur.r = c * per;
+    for (;;) {
+      cur.q.load(a, cur.r, row_limit);
+      head = cur.q.per_head(a);
+      if (begin < at + head * a.c.heads) break;
+      at += head * a.c.heads;
+      if (++cur.r >= a.requests) return;  // not reached: `begin` is inside the list
+    }
+    long long rest = begin - at;
+    cur.h = static_cast<int>(rest / head);
+    rest -= cur.h * head;
+    cur.group = 0;
+    while (rest >= (cur.tiles = cur.q.tiles(a, cur.group))) {
+      rest -= cur.tiles;
+      ++cur.group;
+    }
+    cur.tile = static_cast<int>(rest);
+  }
+  const int count = static_cast<int>(min(end - begin, 0x7fffffffLL));
+
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
+                     shared_u32(tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      bar_init(bar(kKFull, i), 4);
+      bar_init(bar(kKEmpty, i), 1);
+      bar_init(bar(kVFull, i), 4);
+      bar_init(bar(kVEmpty, i), 1);
+      bar_init(bar(kScFree, i), 8);
+      bar_init(bar(kSFull, i), 1);
+      bar_init(bar(kPFull, i), 4);
+      bar_init(bar(kQFull, i), 4);
+      bar_init(bar(kODone, i), 1);
+    }
+    bar_init(bar(kDrain), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    *stop = 0;
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < 8) {
+    // ================ rows: thread (i, lane of the tile) holds one query row
+    const int i = warp >> 2, rt = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_col = tmem + lanes + i * 128, o_col = tmem + lanes + 256 + i * D;
+    const unsigned char* scales = chunk_smem + L::scales;
+    float m = -INFINITY, l = 0.f, qs = 0.f;
+    int see = 0, row = 0;
+    // this row's queries to shared memory, scaled by a power of two so that halves hold them
+    auto load_q = [&]() {
+      row = cur.group * kRows + i * 128 + rt;
+      m = -INFINITY;
+      l = 0.f;
+      see = 0;
+      float top = 0.f;
+      const bool on = row < cur.q.rows;
+      const uint4* p = nullptr;
+      if (on) {
+        const int tok = row / a.group;
+        see = static_cast<int>(max(min(static_cast<long long>(cur.q.ctx) + tok + 1,
+                                       static_cast<long long>(cur.q.see)), 0LL));
+        p = reinterpret_cast<const uint4*>(
+            static_cast<const uint16_t*>(a.q) + (cur.q.q_lo + tok) * a.q_token_stride +
+            (cur.h * a.group + (row - tok * a.group)) * a.q_head_stride);
+        for (int c = 0; c < kCols; ++c) {
+          const uint4 w = __ldg(p + c);
+          float y[8];
+          if (a.fp16) unpack8<ALHR_TYPE_FP16>(w, w, y);
+          else unpack8<ALHR_TYPE_BF16>(w, w, y);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(y[j]));
+        }
+      }
+      const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100), 126);
+      // a negative factor of the scores goes into the queries: what follows takes the largest
+      // score as the largest product
+      const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23),
+                                 a.scale_log2);
+      qs = __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23) * fabsf(a.scale_log2);
+      const uint32_t dst = smem + L::q + i * L::kTile + (rt >> 3) * (kCols * 128) + (rt & 7) * 16;
+      for (int c = 0; c < kCols; ++c) {
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (on) {
+          w = __ldg(p + c);
+          float y[8];
+          if (a.fp16) unpack8<ALHR_TYPE_FP16>(w, w, y);
+          else unpack8<ALHR_TYPE_BF16>(w, w, y);
+          w = make_uint4(pack2(y[0] * up, y[1] * up, true), pack2(y[2] * up, y[3] * up, true),
+                         pack2(y[4] * up, y[5] * up, true), pack2(y[6] * up, y[7] * up, true));
+        }
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(dst + c * 128), "r"(w.x),
+                     "r"(w.y), "r"(w.z), "r"(w.w)
+                     : "memory");
+      }
+      fence_shared();
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar(kQFull, i));
+    };
+    bool first = true, from_start = cur.tile == 0;
+    int units = 0;
+    bool busy = cur.rows_here() > i * 128;  // the second tile of rows may be empty
+    if (busy) load_q();
+    uint32_t s_phase = 0;
+    for (int j = 0; j < count; ++j) {
+      const int b = j & 1;
+      if (!warp_wait(bar(kKFull, b), (j >> 1) & 1, stop)) break;
+      const bool last = cur.tile + 1 == cur.tiles || j + 1 == count;
+      if (!busy) {
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar(kScFree, b));
+      } else {
+        if (!warp_wait(bar(kSFull, i), s_phase, stop)) break;
+        s_phase ^= 1u;
+        fence_after();
+        const int seen = see - cur.tile * kKeys;  // columns < seen are visible
+        const bool cut = __any_sync(0xffffffffu, seen < kKeys);
+        const float4* sc = reinterpret_cast<const float4*>(scales) + b * 8;
+        // the largest x of the row
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tmem_ld32(v, s_col + c * 32);
+          wait_ld();
+          if (cut) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (c * 32 + k >= seen) v[k] = 0xff800000u;  // -infinity
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float x = __uint_as_float(v[u * 16]);
+#pragma unroll
+            for (int k = 1; k < 16; ++k) x = fmaxf(x, __uint_as_float(v[u * 16 + k]));
+            const float4 f = sc[c * 2 + u];
+            // -infinity stays where the factor is 0
+            top = fmaxf(top, x == -INFINITY ? x : fmaf(x, qs * f.x, f.y));
+          }
+        }
+        const bool grow = top > m + kTopLog + 8.f;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float mn = fmaxf(m, top - kTopLog);
+          const float keep = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
+          m = mn;
+          l *= keep;
+          if (!first) {
+            // the product before this tile's scores is complete: they were issued after it
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t v[32];
+              tmem_ld32(v, o_col + c * 32);
+              wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * keep);
+              tmem_st32(o_col + c * 32, v);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32], p[16];
+          tmem_ld32(v, s_col + c * 32);
+          wait_ld();
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float4 f = sc[c * 2 + u];
+            const float f1 = qs * f.x, f0 = f.y - base;
+            float part = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              float x0 = exp2_fast(fmaf(__uint_as_float(v[u * 16 + k]), f1, f0));
+              float x1 = exp2_fast(fmaf(__uint_as_float(v[u * 16 + k + 1]), f1, f0));
+              if (cut) {
+                if (c * 32 + u * 16 + k >= seen) x0 = 0.f;
+                if (c * 32 + u * 16 + k + 1 >= seen) x1 = 0.f;
+              }
+              part += x0 + x1;
+              p[u * 8 + k / 2] = pack2(x0, x1, true);
+            }
+            l = fmaf(part, f.z, l);
+          }
+          tmem_st16(s_col + c * 16, p);
+        }
+        wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(bar(kScFree, b));
+          bar_arrive(bar(kPFull, i));
+        }
+      }
+      first = false;
+      if (!last) {
+        ++cur.tile;
+        continue;
+      }
+      // ---- the unit (or this piece of it) ends
+      const ChunkCursor was = cur;
+      const int was_row = row;
+      const float was_m = m, was_l = l;
+      const bool was_busy = busy, to_end = cur.tile + 1 == cur.tiles, started = from_start;
+      first = from_start = true;
+      if (j + 1 < count) {
+        cur.step(a, row_limit);
+        busy = cur.rows_here() > i * 128;
+        // S of the last tile is here, so nothing reads this tile of queries any more
+        if (busy) load_q();
+      }
+      if (was_busy) {
+        if (!warp_wait(bar(kODone, i), units & 1, stop)) break;
+        ++units;
+        fence_after();
+        const bool on = was_row < was.q.rows;
+        const int tok = was_row / a.group;
+        const long long at = static_cast<long long>(was.q.q_lo + tok) * a.q_heads +
+                             was.h * a.group + (was_row - tok * a.group);
+        const float inv = was_l > 0.f ? 1.f / was_l : 0.f;
+        float* part = space.part + (static_cast<long long>(piece) * 2 + (started ? 1 : 0)) *
+                                       (kRows * (D + 2));
+        const int pr = i * 128 + rt;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(v, o_col + c * 32);
+          wait_ld();
+          if (on && started && to_end) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D + c * 32);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack2(__uint_as_float(v[k * 8 + 2 * e]) * inv,
+                             __uint_as_float(v[k * 8 + 2 * e + 1]) * inv, a.fp16);
+              dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else if (on) {
+            uint4* dst = reinterpret_cast<uint4*>(part + pr * D + c * 32);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          }
+          __syncwarp();
+        }
+        if (on && started && to_end) {
+          if (a.lse)
+            a.lse[at] = was_l > 0.f ? (was_m + log2f(was_l)) * 0.6931471805599453f : -INFINITY;
+        } else if (on) {
+          part[kRows * D + pr] = was_m;
+          part[kRows * D + kRows + pr] = was_l;
+        }
+        fence_before();
+      }
+      if (tid == 0 && started && !to_end) {
+        meta->r = was.r;
+        meta->h = was.h;
+        meta->row0 = was.group * kRows;
+        meta->rows = was.rows_here();
+        meta->last = split.piece_of(end - 1 + (was.tiles - 1 - was.tile));
+      }
+    }
+  } else if (warp < 12) {
+    // ================ keys and values: codes to halves
+    const int w = warp - 8;
+    const int kr = lane & 7, kc = lane >> 3;       // row of eight, 16-byte piece of 64
+    constexpr int kHalves = D / 64;                // pieces kc, kc + 4
+    bool bad = false;
+    ChunkCursor next = cur;                        // the tile whose codes are asked for
+    // blocks of the two 16-key groups of this warp's 32 keys
+    auto blocks_of = [&](const ChunkCursor& c, int (&blk)[2]) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int key = c.tile * kKeys + w * 32 + u * 16;
+        blk[u] = -1;
+        if (key < c.q.see) {
+          blk[u] = __ldg(a.table + static_cast<long long>(c.r) * a.max_blocks + (key >> a.c.bs_log));
+          if (blk[u] < 0 || blk[u] >= a.c.blocks) {
+            blk[u] = -1;
+            bad = true;
+          }
+        }
+      }
+    };
+    auto fetch = [&](const uint8_t* codes, const ChunkCursor& c, const int (&blk)[2],
+                     uint4 (&raw)[4 * kHalves]) {
+#pragma unroll
+      for (int rg = 0; rg < 4; ++rg) {
+        const int key = c.tile * kKeys + w * 32 + rg * 8 + kr;
+        const int block = blk[rg >> 1];
+        const bool on = block >= 0 && key < c.q.see;
+        const long long row = block_row(a.c, max(block, 0), c.h) + (key & (a.c.bs - 1));
+        const uint4* p = reinterpret_cast<const uint4*>(codes + row * D + kc * 16);
+#pragma unroll
+        for (int hh = 0; hh < kHalves; ++hh)
+          raw[rg * kHalves + hh] = on ? __ldg(p + hh * 4) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    auto widen = [&](uint32_t dst, const uint4 (&raw)[4 * kHalves]) {
+#pragma unroll
+      for (int rg = 0; rg < 4; ++rg)
+#pragma unroll
+        for (int hh = 0; hh < kHalves; ++hh) {
+          const uint4 x = raw[rg * kHalves + hh];
+          uint32_t y[8];
+          widen4<CODE>(x.x, y[0], y[1]);
+          widen4<CODE>(x.y, y[2], y[3]);
+          widen4<CODE>(x.z, y[4], y[5]);
+          widen4<CODE>(x.w, y[6], y[7]);
+          const uint32_t at = dst + ((w * 4 + rg) * kCols + (kc + hh * 4) * 2) * 128 + kr * 16;
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(at), "r"(y[0]), "r"(y[1]),
+                       "r"(y[2]), "r"(y[3])
+                       : "memory");
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(at + 128), "r"(y[4]),
+                       "r"(y[5]), "r"(y[6]), "r"(y[7])
+                       : "memory");
+        }
+    };
+    uint4 raw_k[4 * kHalves], raw_v[4 * kHalves];
+    int blk[2], blk_next[2] = {-1, -1};
+    blocks_of(next, blk);
+    fetch(a.c.k, next, blk, raw_k);
+    fetch(a.c.v, next, blk, raw_v);
+    ChunkCursor at = next;
+    if (count > 1) {
+      next.step(a, row_limit);
+      blocks_of(next, blk_next);
+    }
+    for (int j = 0; j < count; ++j) {
+      const int b = j & 1;
+      // lanes 0, 1: scales of this warp's groups
+      float ks = 0.f, vs = 0.f;
+      const int mine = lane == 0 ? blk[0] : blk[1];
+      if (lane < 2 && mine >= 0) {
+        const long long si = static_cast<long long>(mine) * a.c.heads + at.h;
+        ks = __ldg(a.c.k_scale + si);
+        vs = __ldg(a.c.v_scale + si);
+      }
+      if (j >= 2) {
+        if (!warp_wait(bar(kKEmpty, b), ((j >> 1) - 1) & 1, stop)) break;
+        if (!warp_wait(bar(kScFree, b), ((j >> 1) - 1) & 1, stop)) break;
+      }
+      widen(smem + L::k + b * L::kTile, raw_k);
+      if (lane < 2) {
+        const float v1 = fmaxf(vs, kTinyScale);
+        float4 f = make_float4(ks, __log2f(v1), __frcp_rn(v1), 0.f);
+        if (mine < 0) f = make_float4(0.f, -INFINITY, 0.f, 0.f);
+        reinterpret_cast<float4*>(chunk_smem + L::scales)[b * 8 + w * 2 + lane] = f;
+      }
+      fence_shared();
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar(kKFull, b));
+      if (j + 1 < count) fetch(a.c.k, next, blk_next, raw_k);
+      if (j >= 2 && !warp_wait(bar(kVEmpty, b), ((j >> 1) - 1) & 1, stop)) break;
+      widen(smem + L::v + b * L::kTile, raw_v);
+      fence_shared();
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar(kVFull, b));
+      if (j + 1 < count) {
+        fetch(a.c.v, next, blk_next, raw_v);
+        blk[0] = blk_next[0];
+        blk[1] = blk_next[1];
+        at = next;
+        if (j + 2 < count) {
+          next.step(a, row_limit);
+          blocks_of(next, blk_next);
+        }
+      }
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) cache_flag(a.dev_err, ALHR_DEVERR_BLOCK);
+  } else if (warp == 12 && lane == 0) {
+    // ================ products
+    constexpr uint32_t kRowGroup = kCols * 128;  // bytes between groups of eight rows
+    constexpr uint32_t kScore = product_desc(128, false), kSum = product_desc(D, true);
+    auto scores = [&](int i, int b) {
+      const uint32_t qa = smem + L::q + i * L::kTile, ka = smem + L::k + b * L::kTile;
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s)
+        product_ss(tmem + i * 128, operand_desc(qa + s * 256, 128, kRowGroup),
+                   operand_desc(ka + s * 256, 128, kRowGroup), kScore, s > 0);
+    };
+    auto sums = [&](int i, int b, bool add) {
+      const uint32_t va = smem + L::v + b * L::kTile;
+#pragma unroll
+      for (int s = 0; s < kKeys / 16; ++s)
+        product_ts(tmem + 256 + i * D, tmem + i * 128 + s * 8,
+                   operand_desc(va + s * 2 * kRowGroup, kRowGroup, 128), kSum, add || s > 0);
+    };
+    bool ok = true;
+    uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+    // tile j's scores for both tiles of rows are asked for while tile j - 1 is summed
+    int subs = cur.rows_here() > 128 ? 2 : 1;
+    auto ask = [&](int i, int j, bool fresh) {
+      if (fresh) {
+        if (!bar_wait(bar(kQFull, i), q_phase[i], stop)) return false;
+        q_phase[i] ^= 1u;
+      }
+      if (!bar_wait(bar(kKFull, j & 1), (j >> 1) & 1, stop)) return false;
+      fence_after();
+      scores(i, j & 1);
+      commit_to(bar(kSFull, i));
+      return true;
+    };
+    for (int i = 0; i < subs && ok; ++i) ok = ask(i, 0, true);
+    if (ok) commit_to(bar(kKEmpty, 0));
+    bool add = false;
+    for (int j = 0; j < count && ok; ++j) {
+      const bool last = cur.tile + 1 == cur.tiles || j + 1 == count;
+      ChunkCursor after = cur;
+      if (j + 1 < count) after.step(a, row_limit);
+      const int subs_after = after.rows_here() > 128 ? 2 : 1;
+      for (int i = 0; i < 2 && ok; ++i) {
+        if (i < subs) {
+          ok = bar_wait(bar(kPFull, i), p_phase[i], stop);
+          p_phase[i] ^= 1u;
+          if (ok && i == 0) ok = bar_wait(bar(kVFull, j & 1), (j >> 1) & 1, stop);
+          if (!ok) break;
+          fence_after();
+          sums(i, j & 1, add);
+          if (last) commit_to(bar(kODone, i));
+        }
+        if (i == subs - 1) commit_to(bar(kVEmpty, j & 1));
+        if (j + 1 < count && i < subs_after) {
+          ok = ask(i, j + 1, last);
+          if (ok && i == subs_after - 1) commit_to(bar(kKEmpty, (j + 1) & 1));
+        }
+      }
+      add = !last;
+      cur = after;
+      subs = subs_after;
+    }
+    if (!ok) {  // products in flight end before the tensor memory is freed
+      commit_to(bar(kDrain));
+      *stop = 0;
+      bar_wait(bar(kDrain), 0, stop);
+      *stop = 1;
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (tid == 0 && *stop) cache_flag(a.dev_err, ALHR_DEVERR_TIMEOUT);
+  if (warp == 12)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512)
+                 : "memory");
+}
+
+template <int D, int CODE>
+cudaError_t chunk_as(const AttendArgs& a, int sms, int row_limit, void* workspace,
+                     cudaStream_t st) {
+  static thread_local bool configured[128] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 128 || !configured[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        chunk_kernel<D, CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkSmem<D>::bytes);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 128) configured[dev] = true;
+  }
+  JoinSpace space = join_space(workspace, sms);
+  chunk_kernel<D, CODE><<<sms, kChunkThreads, ChunkSmem<D>::bytes, st>>>(a, space, row_limit);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  join_kernel<D, kRows><<<dim3(sms, kRows / kJoinRows), kJoinRows * 32, 0, st>>>(a, space);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t chunk_workspace(int sms, int d) { return join_bytes(sms, kRows, d); }
+
+// Requests of more than row_limit rows (of one key head).
+cudaError_t launch_chunk(const AttendArgs& a, int d, int code, int sms, int row_limit,
+                         void* workspace, cudaStream_t st) {
+  if (d == 64)
+    return code == ALHR_CODE_INT8 ? chunk_as<64, ALHR_CODE_INT8>(a, sms, row_limit, workspace, st)
+                                  : chunk_as<64, ALHR_CODE_E4M3>(a, sms, row_limit, workspace, st);
+  return code == ALHR_CODE_INT8 ? chunk_as<128, ALHR_CODE_INT8>(a, sms, row_limit, workspace, st)
+                                : chunk_as<128, ALHR_CODE_E4M3>(a, sms, row_limit, workspace, st);
+}
+
+}  // namespace alhr

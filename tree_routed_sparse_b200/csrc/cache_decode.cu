@@ -15,9 +15,7 @@
 // in registers and uses the warp-wide matrix product. A unit inside one warp's piece is written at
 // once; one that spans pieces leaves partial sums (O, M, l), which a second kernel joins in the
 // order of the pieces.
-#include <cmath>
-
-#include "cache_mma.cuh"
+#include "cache_split.cuh"
 
 namespace alhr {
 
@@ -50,34 +48,16 @@ __device__ __forceinline__ int piece_offset(int row, int c) {
   return D == 128 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
 }
 
-struct Partial {
-  int unit_r, unit_h, unit_rows0, rows;  // of the unit that starts here and ends elsewhere
-  int last;                              // the piece that ends it; -1: none
-};
-
-// Which pieces of the tile list there are.
-struct Split {
-  long long tiles;
-  int pieces;
-  __device__ __forceinline__ long long first(int i) const { return tiles * i / pieces; }
-  __device__ __forceinline__ int piece_of(long long tile) const {
-    return static_cast<int>(((tile + 1) * pieces - 1) / tiles);
-  }
-};
-
 // One request as the list sees it.
 template <int D, int ROWS>
 struct Request {
   int q_lo, rows, ctx, see, tiles, groups;
   __device__ __forceinline__ void load(const AttendArgs& a, int r, int row_limit) {
-    q_lo = min(max(__ldg(a.q_start + r), 0), a.tokens);
-    const int q_hi = min(max(__ldg(a.q_start + r + 1), q_lo), a.tokens);
-    ctx = __ldg(a.ctx_len + r);
-    const long long cap = static_cast<long long>(a.max_blocks) << a.c.bs_log;
-    const long long end = min(min(static_cast<long long>(ctx) + (q_hi - q_lo),
-                                  static_cast<long long>(__ldg(a.seq_len + r))), cap);
-    see = static_cast<int>(max(end, 0LL));
-    rows = (q_hi - q_lo) * a.group;
+    const RequestRange q(a, r);
+    q_lo = q.q_lo;
+    ctx = q.ctx;
+    see = q.see;
+    rows = q.tokens * a.group;
     groups = rows > row_limit ? 0 : (rows + ROWS - 1) / ROWS;
     tiles = max(1, (see + Tile<D>::kKeys - 1) / Tile<D>::kKeys);
   }
@@ -107,15 +87,6 @@ struct Cursor {
   }
 };
 
-// Floats of one partial: O [ROWS][D], M [ROWS], l [ROWS].
-template <int D, int ROWS>
-constexpr int partial_floats() { return ROWS * (D + 2); }
-
-struct DecodeSpace {
-  Partial* meta;  // [pieces]
-  float* part;    // [pieces][2][partial_floats]: a unit begun earlier, a unit begun here
-};
-
 __device__ __forceinline__ float group_max(float v) {  // over the lanes of equal lane % 4
 #pragma unroll
   for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -129,14 +100,14 @@ __device__ __forceinline__ float group_add(float v) {
 
 template <int D, int CODE, int NT>
 __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
-    decode_kernel(const AttendArgs a, const DecodeSpace space, const int row_limit) {
+    decode_kernel(const AttendArgs a, const JoinSpace space, const int row_limit) {
   constexpr int ROWS = 8 * NT;
   constexpr int KS = D / 16;              // products over d of one 16-key group
   constexpr int SUBS = Tile<D>::kSubs;
   constexpr int LPR = D / 16;             // 16-byte pieces of a row
   constexpr int RPI = 32 / LPR;           // rows one copy of the warp covers
   extern __shared__ __align__(128) unsigned char decode_smem[];
-  __shared__ long long chunk_start[kDecodeWarps * 32 + 1];
+  __shared__ long long chunk_start[kDecodeWarps * 32];
   __shared__ long long warp_sum[kDecodeWarps];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -150,46 +121,21 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
     load.q.load(a, r, row_limit);
     sum += load.q.work(a.c.heads);
   }
-  long long incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += u;
-  }
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
-  long long before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kDecodeWarps; ++w) {
-    before += w < warp ? warp_sum[w] : 0;
-    all += warp_sum[w];
-  }
-  chunk_start[tid] = before + incl - sum;
-  if (tid == 0) chunk_start[kDecodeWarps * 32] = all;
-  __syncthreads();
-
-  // a short list is cut into single tiles, so that every piece it has holds one at least
-  const long long most = static_cast<long long>(gridDim.x) * kDecodeWarps;
-  const Split split{all, static_cast<int>(min(most, all))};
+  const Split split = make_split<kDecodeWarps * 32>(sum, chunk_start, warp_sum,
+                                                    static_cast<long long>(gridDim.x) * kDecodeWarps);
   // pieces beside one another in the list lie on different multiprocessors
   const int piece = warp * gridDim.x + blockIdx.x;
   const long long begin = piece < split.pieces ? split.first(piece) : 0;
   const long long end = piece < split.pieces ? split.first(piece + 1) : 0;
-  Partial* meta = space.meta + piece;
+  JoinMeta* meta = space.meta + piece;
   if (lane == 0) meta->last = -1;
   if (begin >= end) return;
 
   // ---- where this piece begins
   {
-    int lo = 0, hi = kDecodeWarps * 32 - 1;  // the last chunk that starts at or before `begin`
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (chunk_start[mid] <= begin) lo = mid;
-      else hi = mid - 1;
-    }
-    // chunks without work share their start with the next one: the last of them has the work
-    long long at = chunk_start[lo];
-    load.r = lo * per;
+    const int c = chunk_of<kDecodeWarps * 32>(chunk_start, begin);
+    long long at = chunk_start[c];
+    load.r = c * per;
     for (;;) {
       load.q.load(a, load.r, row_limit);
       const long long w = load.q.work(a.c.heads);
@@ -362,7 +308,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
             a.lse[at] = sum_l > 0.f ? (m[n][c] + log2f(sum_l)) * 0.6931471805599453f : -INFINITY;
         } else {
           float* part = space.part + (static_cast<long long>(piece) * 2 + (from_start ? 1 : 0)) *
-                                         partial_floats<D, ROWS>();
+                                         (ROWS * (D + 2));
           float4* p = reinterpret_cast<float4*>(part + col * D + g * (D / 8));
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
@@ -375,9 +321,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
       }
     }
     if (from_start && !to_end && lane == 0) {
-      meta->unit_r = cur.r;
-      meta->unit_h = cur.h;
-      meta->unit_rows0 = row0;
+      meta->r = cur.r;
+      meta->h = cur.h;
+      meta->row0 = row0;
       meta->rows = min(ROWS, cur.q.rows - row0);
       // the unit's last tile: this piece ends inside the unit, at list position `end`
       meta->last = split.piece_of(end - 1 + (cur.q.tiles - 1 - cur.tile));
@@ -544,50 +490,6 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
   if (__any_sync(0xffffffffu, bad) && lane == 0) cache_flag(a.dev_err, ALHR_DEVERR_BLOCK);
 }
 
-// Joins the partial sums of the units that span pieces: one CTA for each piece in which such a
-// unit begins, one warp a row.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(ROWS * 32) decode_join_kernel(const AttendArgs a,
-                                                                const DecodeSpace space) {
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int piece = blockIdx.x, lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-  const Partial p = space.meta[piece];
-  if (p.last < 0 || row >= p.rows) return;
-  constexpr int E = D / 32;
-  constexpr int kStep = partial_floats<D, ROWS>();
-  // partials: slot 1 of this piece, slot 0 of the pieces behind it
-  const int n = p.last - piece + 1;
-  auto part = [&](int i) {
-    return space.part + (static_cast<long long>(piece + i) * 2 + (i == 0 ? 1 : 0)) * kStep;
-  };
-  float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, part(i)[ROWS * D + row]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float base = m == -INFINITY ? 0.f : m;
-  float acc[E], l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* x = part(i);
-    const float f = exp2_fast(x[ROWS * D + row] - base);
-    l = fmaf(x[ROWS * D + ROWS + row], f, l);
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(x[row * D + lane * E + e], f, acc[e]);
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const int rr = p.unit_rows0 + row, tok = rr / a.group;
-  const int q_lo = min(max(__ldg(a.q_start + p.unit_r), 0), a.tokens);
-  const long long at = static_cast<long long>(q_lo + tok) * a.q_heads + p.unit_h * a.group +
-                       (rr - tok * a.group);
-#pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at * D + lane * E + e) =
-        pack2(acc[e] * inv, acc[e + 1] * inv, a.fp16);
-  if (a.lse && lane == 0) a.lse[at] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-}
-
 template <int D, int CODE, int NT>
 cudaError_t decode_as(const AttendArgs& a, int sms, int row_limit, cudaStream_t st) {
   static thread_local bool configured[128] = {};
@@ -601,20 +503,18 @@ cudaError_t decode_as(const AttendArgs& a, int sms, int row_limit, cudaStream_t 
     if (dev >= 0 && dev < 128) configured[dev] = true;
   }
   const int pieces = sms * kDecodeWarps;
-  DecodeSpace space;
-  space.meta = static_cast<Partial*>(a.workspace);
-  space.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + pieces * 32);
+  const JoinSpace space = join_space(a.workspace, pieces);
   decode_kernel<D, CODE, NT><<<sms, kDecodeWarps * 32, kSmem, st>>>(a, space, row_limit);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  decode_join_kernel<D, 8 * NT><<<pieces, 8 * NT * 32, 0, st>>>(a, space);
+  join_kernel<D, 8 * NT><<<dim3(pieces, NT), kJoinRows * 32, 0, st>>>(a, space);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t decode_workspace(int sms, int d) {
-  return static_cast<size_t>(sms) * kDecodeWarps * (32 + 2 * 16 * (d + 2) * sizeof(float));
+  return join_bytes(sms * kDecodeWarps, 16, d);
 }
 
 // Requests of at most row_limit rows (of one key head).

@@ -1,0 +1,136 @@
+// cache_split.cuh -- equal pieces of one list of key tiles, and the join of the units they cut.
+#pragma once
+
+#include <cmath>
+
+#include "cache_mma.cuh"
+
+namespace alhr {
+
+// Rows and visible keys of one request, inside the arrays whatever the device memory holds.
+struct RequestRange {
+  int q_lo, tokens, ctx, see;
+  __device__ __forceinline__ RequestRange(const AttendArgs& a, int r) {
+    q_lo = min(max(__ldg(a.q_start + r), 0), a.tokens);
+    tokens = min(max(__ldg(a.q_start + r + 1), q_lo), a.tokens) - q_lo;
+    ctx = __ldg(a.ctx_len + r);
+    const long long cap = static_cast<long long>(a.max_blocks) << a.c.bs_log;
+    const long long end = min(min(static_cast<long long>(ctx) + tokens,
+                                  static_cast<long long>(__ldg(a.seq_len + r))), cap);
+    see = static_cast<int>(max(end, 0LL));
+  }
+};
+
+// `tiles` tiles in `pieces` pieces: piece i begins at tile first(i).
+struct Split {
+  long long tiles;
+  int pieces;
+  __device__ __forceinline__ long long first(int i) const { return tiles * i / pieces; }
+  __device__ __forceinline__ int piece_of(long long tile) const {
+    return static_cast<int>(((tile + 1) * pieces - 1) / tiles);
+  }
+};
+
+// The list of a CTA whose thread t has `mine` tiles (a run of requests): start[t] is where they
+// begin. A short list is cut into single tiles, so that every piece it has holds one at least.
+template <int THREADS>
+__device__ __forceinline__ Split make_split(long long mine, long long* start, long long* warp_sum,
+                                            long long most_pieces) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    before += w < warp ? warp_sum[w] : 0;
+    all += warp_sum[w];
+  }
+  start[threadIdx.x] = before + incl - mine;
+  __syncthreads();
+  return Split{all, static_cast<int>(min(most_pieces, all))};
+}
+
+// The last thread whose tiles begin at or before `tile`: threads without any share their start
+// with the next one, so that it has some.
+template <int THREADS>
+__device__ __forceinline__ int chunk_of(const long long* start, long long tile) {
+  int lo = 0, hi = THREADS - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start[mid] <= tile) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// A unit that begins in a piece and ends in a later one: its rows, and the piece that ends it
+// (-1: the piece has no such unit).
+struct JoinMeta {
+  int r, h, row0, rows, last;
+};
+
+struct JoinSpace {
+  JoinMeta* meta;  // [pieces]
+  float* part;     // [pieces][2] of O [ROWS][D], M [ROWS], l [ROWS]: of a unit that began in an
+                   // earlier piece, of one that begins here
+};
+
+inline size_t join_bytes(int pieces, int rows, int d) {
+  return static_cast<size_t>(pieces) * (32 + 2 * static_cast<size_t>(rows) * (d + 2) * sizeof(float));
+}
+inline JoinSpace join_space(void* workspace, int pieces) {
+  return JoinSpace{static_cast<JoinMeta*>(workspace),
+                   reinterpret_cast<float*>(static_cast<char*>(workspace) + pieces * 32)};
+}
+
+constexpr int kJoinRows = 8;
+
+// Joins the partial sums in the order of the pieces: grid (pieces, ROWS / kJoinRows), one warp a
+// row, weights 2^(M_i - max M).
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kJoinRows * 32) join_kernel(const AttendArgs a,
+                                                              const JoinSpace space) {
+  const int piece = blockIdx.x, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+  const JoinMeta p = space.meta[piece];
+  if (p.last < 0 || row >= p.rows) return;
+  constexpr int E = D / 32, kStep = ROWS * (D + 2);
+  const int n = p.last - piece + 1;
+  auto part = [&](int i) {
+    return space.part + (static_cast<long long>(piece + i) * 2 + (i == 0 ? 1 : 0)) * kStep;
+  };
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, part(i)[ROWS * D + row]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float base = m == -INFINITY ? 0.f : m;
+  float acc[E], l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float* x = part(i);
+    const float f = exp2_fast(x[ROWS * D + row] - base);
+    l = fmaf(x[ROWS * D + ROWS + row], f, l);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(x[row * D + lane * E + e], f, acc[e]);
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int rr = p.row0 + row, tok = rr / a.group;
+  const int q_lo = min(max(__ldg(a.q_start + p.r), 0), a.tokens);
+  const long long at = static_cast<long long>(q_lo + tok) * a.q_heads + p.h * a.group +
+                       (rr - tok * a.group);
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at * D + lane * E + e) =
+        pack2(acc[e] * inv, acc[e + 1] * inv, a.fp16);
+  if (a.lse && lane == 0) a.lse[at] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+}  // namespace alhr
