@@ -1,98 +1,163 @@
 // cache_store.cu -- new tokens into the paged 8-bit cache, and its numbers back.
 //
+// Both are bound by memory: a stored number is read once (2 bytes) and written once (1 byte), a
+// loaded one the other way round.
+//
 // store: one warp takes one run (rows of consecutive slots of one block) of one head, keys or
 // values: the run's largest magnitude, the block's new scale, the codes of the rows before the run
-// if the scale grew, the codes of the run. Each pass covers 32 / (d / 8) rows, eight numbers a
-// lane.
-#include "cache_device.cuh"
+// if the scale grew, the codes of the run. A pass covers 32 / (d / 8) rows, eight numbers a lane;
+// the first eight passes stay in registers between the maximum and the codes, the rest are read
+// again (from L2). The quotient x / s is one rounding of the exact one, by Markstein's correction
+// of x * (1 / s) (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990): three operations where a division takes about ten.
+#include "cache_mma.cuh"
 
 namespace alhr {
 
 namespace {
 
 constexpr int kStoreWarps = 4;
+constexpr int kKept = 8;
 
 template <int T>
-__device__ __forceinline__ void load8(const void* base, long long at, float (&x)[8]) {
-  if constexpr (T == ALHR_TYPE_FP32) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + at);
-    unpack8<T>(__ldg(p), __ldg(p + 1), x);
-  } else {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
-    unpack8<T>(a, a, x);
+struct Raw8 {
+  uint4 a[T == ALHR_TYPE_FP32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* base, long long at) {
+    if constexpr (T == ALHR_TYPE_FP32) {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + at);
+      a[0] = __ldg(p);
+      a[1] = __ldg(p + 1);
+    } else {
+      a[0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
+    }
   }
-}
+  __device__ __forceinline__ void numbers(float (&x)[8]) const {
+    unpack8<T>(a[0], a[T == ALHR_TYPE_FP32 ? 1 : 0], x);
+  }
+};
 
+// Eight finite numbers as codes: nearest, ties to even, saturated.
 template <int CODE>
 __device__ __forceinline__ uint2 encode8(const float (&x)[8]) {
-  uint32_t w[2] = {0u, 0u};
+  uint32_t w[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    w[i >> 2] |= static_cast<uint32_t>(encode<CODE>(x[i])) << (8 * (i & 3));
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (CODE == ALHR_CODE_INT8) {
+      // x + 1.5 * 2^23 holds the rounded number in its low bits
+      uint32_t c[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        c[j] = __float_as_uint(fminf(fmaxf(x[4 * i + j], -127.f), 127.f) + 12582912.f);
+      w[i] = prmt(prmt(c[0], c[1], 0x0040), prmt(c[2], c[3], 0x0040), 0x5410);
+    } else {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i], x[4 * i + 1]),
+                                                   __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2], x[4 * i + 3]),
+                                                   __NV_SATFINITE, __NV_E4M3);
+      w[i] = lo | (hi << 16);
+    }
+  }
   return make_uint2(w[0], w[1]);
 }
 
+// Any numbers: infinities saturate, NaN becomes 0.
 template <int CODE>
-__device__ __forceinline__ void decode8(const uint2& c, float (&x)[8]) {
+__device__ __noinline__ uint2 encode8_any(float (&x)[8], float s) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    x[i] = decode<CODE>(static_cast<uint8_t>((i < 4 ? c.x : c.y) >> (8 * (i & 3))));
+  for (int j = 0; j < 8; ++j) {
+    x[j] = __fdiv_rn(x[j], s);
+    x[j] = x[j] != x[j] ? 0.f : fminf(fmaxf(x[j], -448.f), 448.f);
+  }
+  return encode8<CODE>(x);
 }
 
+template <int CODE>
+__device__ __forceinline__ void decode4(uint32_t w, float* x) {
+  uint32_t lo, hi;
+  widen4<CODE>(w, lo, hi);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+}
+
+// per: tokens a warp looks through for the beginnings of runs.
 template <int D, int CODE, int T>
-__global__ void __launch_bounds__(kStoreWarps * 32) store_kernel(const StoreArgs a) {
+__global__ void __launch_bounds__(kStoreWarps * 32) store_kernel(const StoreArgs a, const int per) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes a row, rows a pass
   constexpr float kFull = CODE == ALHR_CODE_INT8 ? 127.f : 256.f;
   const int lane = threadIdx.x & 31;
   const int bs = a.c.bs, heads = a.c.heads;
   const long long slots_end = static_cast<long long>(a.c.blocks) << a.c.bs_log;
-  const long long units = static_cast<long long>(a.tokens) * heads * 2;
-  for (long long u = static_cast<long long>(blockIdx.x) * kStoreWarps + (threadIdx.x >> 5);
-       u < units; u += static_cast<long long>(gridDim.x) * kStoreWarps) {
-    const int t = static_cast<int>(u / (2 * heads));
-    const int hw = static_cast<int>(u - static_cast<long long>(t) * 2 * heads);
-    const int which = hw >= heads, h = hw - which * heads;
-    const long long slot = __ldg(a.slots + t);
+  // blockIdx.y, warp: head, keys or values; blockIdx.x: tokens
+  const int hw = blockIdx.y * kStoreWarps + (threadIdx.x >> 5);
+  if (hw >= 2 * heads) return;
+  const int which = hw >= heads, h = hw - which * heads;
+  const void* const x = a.x[which];
+  const long long step = a.token_stride[which];
+  const int sub = lane % kLanes, row = lane / kLanes;
+  const long long t0 = static_cast<long long>(blockIdx.x) * per;
+  const int look = static_cast<int>(min(static_cast<long long>(per), a.tokens - t0));
+
+  // lane i: does a run begin at token t0 + i
+  long long slot = -1;
+  bool leads = false;
+  if (lane < look) {
+    slot = __ldg(a.slots + t0 + lane);
     if (slot < 0 || slot >= slots_end) {
-      if (slot != -1 && lane == 0) cache_flag(a.dev_err, ALHR_DEVERR_BLOCK);
-      continue;
+      if (slot != -1) cache_flag(a.dev_err, ALHR_DEVERR_BLOCK);
+    } else {
+      leads = (slot & (bs - 1)) == 0 || t0 + lane == 0 || __ldg(a.slots + t0 + lane - 1) + 1 != slot;
     }
-    const int off = static_cast<int>(slot & (bs - 1));
-    if (off != 0 && t > 0 && __ldg(a.slots + t - 1) + 1 == slot) continue;  // inside a run
+  }
+  for (unsigned left = __ballot_sync(0xffffffffu, leads); left; left &= left - 1) {
+    const int at = __ffs(left) - 1;
+    const long long s0 = __shfl_sync(0xffffffffu, slot, at);
+    const long long t = t0 + at;
+    const int off = static_cast<int>(s0 & (bs - 1));
     int n = 0;  // rows of the run
-    const int most = min(bs - off, a.tokens - t);
+    const int most = static_cast<int>(min(static_cast<long long>(bs - off), a.tokens - t));
     for (int i = 0; i < most; i += 32) {
-      const bool on = i + lane < most && __ldg(a.slots + t + i + lane) == slot + i + lane;
+      const bool on = i + lane < most && __ldg(a.slots + t + i + lane) == s0 + i + lane;
       const unsigned m = __ballot_sync(0xffffffffu, on);
       n += m == 0xffffffffu ? 32 : __ffs(~m) - 1;
       if (m != 0xffffffffu) break;
     }
-    const int block = static_cast<int>(slot >> a.c.bs_log);
-    const int sub = lane % kLanes, row = lane / kLanes;
-    const void* x = a.x[which];
-    const long long x0 = static_cast<long long>(t) * a.token_stride[which] +
-                         static_cast<long long>(h) * a.head_stride[which] + sub * 8;
-    const long long step = a.token_stride[which];
+    const int block = static_cast<int>(s0 >> a.c.bs_log);
+    const long long x0 = t * step + static_cast<long long>(h) * a.head_stride[which] + sub * 8;
 
+    Raw8<T> kept[kKept];
+#pragma unroll
+    for (int p = 0; p < kKept; ++p)
+      if (p * kRows + row < n) kept[p].load(x, x0 + (p * kRows + row) * step);
     float amax = 0.f;
     bool odd = false;
-    for (int i = row; i < n; i += kRows) {
+    auto largest = [&](const Raw8<T>& r) {
       float v[8];
-      load8<T>(x, x0 + i * step, v);
+      r.numbers(v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float m = fabsf(v[j]);
         if (m <= 3.402823466e38f) amax = fmaxf(amax, m);
         else odd = true;
       }
+    };
+#pragma unroll
+    for (int p = 0; p < kKept; ++p)
+      if (p * kRows + row < n) largest(kept[p]);
+#pragma unroll 4
+    for (int i = kKept * kRows + row; i < n; i += kRows) {
+      Raw8<T> r;
+      r.load(x, x0 + i * step);
+      largest(r);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (__any_sync(0xffffffffu, odd) && lane == 0) cache_flag(a.dev_err, ALHR_DEVERR_NONFINITE);
+    odd = __any_sync(0xffffffffu, odd);
+    if (odd && lane == 0) cache_flag(a.dev_err, ALHR_DEVERR_NONFINITE);
 
     float* scale = (which ? a.c.v_scale : a.c.k_scale) + static_cast<long long>(block) * heads + h;
     const float old = off == 0 ? 0.f : *scale;
-    const float s = fmaxf(fmaxf(old, __fdiv_rn(amax, kFull)), 7.888609052e-31f);  // 2^-100
+    const float s = fmaxf(fmaxf(old, __fdiv_rn(amax, kFull)), kTinyScale);
     uint8_t* codes = (which ? a.c.v : a.c.k) + block_row(a.c, block, h) * D + sub * 8;
     __syncwarp();  // every lane has read the old scale
     if (lane == 0) *scale = s;
@@ -100,82 +165,114 @@ __global__ void __launch_bounds__(kStoreWarps * 32) store_kernel(const StoreArgs
       const float f = __fdiv_rn(old, s);
       for (int i = row; i < off; i += kRows) {
         uint2* p = reinterpret_cast<uint2*>(codes + static_cast<long long>(i) * D);
+        const uint2 c = *p;
         float v[8];
-        decode8<CODE>(*p, v);
+        decode4<CODE>(c.x, v);
+        decode4<CODE>(c.y, v + 4);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], f);
         *p = encode8<CODE>(v);
       }
     }
-    for (int i = row; i < n; i += kRows) {
+    const float inv = __frcp_rn(s);
+    auto put = [&](const Raw8<T>& r, int i) {
       float v[8];
-      load8<T>(x, x0 + i * step, v);
+      r.numbers(v);
+      uint2 c;
+      if (odd) {
+        c = encode8_any<CODE>(v, s);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fdiv_rn(v[j], s);
-      *reinterpret_cast<uint2*>(codes + static_cast<long long>(off + i) * D) = encode8<CODE>(v);
+        for (int j = 0; j < 8; ++j) {
+          const float q = __fmul_rn(v[j], inv);
+          v[j] = __fmaf_rn(__fmaf_rn(-q, s, v[j]), inv, q);
+        }
+        c = encode8<CODE>(v);
+      }
+      *reinterpret_cast<uint2*>(codes + static_cast<long long>(off + i) * D) = c;
+    };
+#pragma unroll
+    for (int p = 0; p < kKept; ++p)
+      if (p * kRows + row < n) put(kept[p], p * kRows + row);
+#pragma unroll 4
+    for (int i = kKept * kRows + row; i < n; i += kRows) {
+      Raw8<T> r;
+      r.load(x, x0 + i * step);
+      put(r, i);
     }
   }
 }
 
+// Threads (piece, token): 16 numbers of one head of one token, keys or values.
 template <int D, int CODE, int T>
 __global__ void __launch_bounds__(256) load_kernel(const LoadArgs a) {
-  constexpr int kLanes = D / 8;
-  const int heads = a.c.heads;
+  constexpr int kPieces = D / 16;
+  const int heads = a.c.heads, all = 2 * heads * kPieces;
   const long long slots_end = static_cast<long long>(a.c.blocks) << a.c.bs_log;
-  const long long units = static_cast<long long>(a.tokens) * heads * 2 * kLanes;
-  bool bad = false;
-  for (long long u = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; u < units;
-       u += static_cast<long long>(gridDim.x) * 256) {
-    const int sub = static_cast<int>(u % kLanes);
-    const long long rest = u / kLanes;
-    const int hw = static_cast<int>(rest % (2 * heads));
-    const long long t = rest / (2 * heads);
+  const int t = blockIdx.x * blockDim.y + threadIdx.y;
+  if (t >= a.tokens) return;
+  const long long slot = __ldg(a.slots + t);
+  const bool there = slot >= 0 && slot < slots_end;
+  if (!there && slot != -1 && threadIdx.x == 0) cache_flag(a.dev_err, ALHR_DEVERR_BLOCK);
+  const int block = there ? static_cast<int>(slot >> a.c.bs_log) : 0;
+  const int off = there ? static_cast<int>(slot & (a.c.bs - 1)) : 0;
+  for (int i = threadIdx.x; i < all; i += blockDim.x) {
+    const int sub = i % kPieces, hw = i / kPieces;
     const int which = hw >= heads, h = hw - which * heads;
-    const long long slot = __ldg(a.slots + t);
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (slot >= 0 && slot < slots_end) {
-      const int block = static_cast<int>(slot >> a.c.bs_log);
-      const int off = static_cast<int>(slot & (a.c.bs - 1));
+    float v[16];
+    if (there) {
       const uint8_t* codes =
-          (which ? a.c.v : a.c.k) + (block_row(a.c, block, h) + off) * D + sub * 8;
+          (which ? a.c.v : a.c.k) + (block_row(a.c, block, h) + off) * D + sub * 16;
       const float s =
           __ldg((which ? a.c.v_scale : a.c.k_scale) + static_cast<long long>(block) * heads + h);
-      decode8<CODE>(__ldg(reinterpret_cast<const uint2*>(codes)), v);
+      const uint4 c = __ldg(reinterpret_cast<const uint4*>(codes));
+      decode4<CODE>(c.x, v);
+      decode4<CODE>(c.y, v + 4);
+      decode4<CODE>(c.z, v + 8);
+      decode4<CODE>(c.w, v + 12);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], s);
-    } else if (slot != -1) {
-      bad = true;
+      for (int j = 0; j < 16; ++j) v[j] = __fmul_rn(v[j], s);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = 0.f;
     }
-    const long long at = (t * heads + h) * D + sub * 8;
+    const long long at = (static_cast<long long>(t) * heads + h) * D + sub * 16;
     if constexpr (T == ALHR_TYPE_FP32) {
       float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.x[which]) + at);
-      p[0] = make_float4(v[0], v[1], v[2], v[3]);
-      p[1] = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
     } else {
       constexpr bool kHalf = T == ALHR_TYPE_FP16;
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.x[which]) + at) =
-          make_uint4(pack2(v[0], v[1], kHalf), pack2(v[2], v[3], kHalf), pack2(v[4], v[5], kHalf),
-                     pack2(v[6], v[7], kHalf));
+      uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.x[which]) + at);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        p[j] = make_uint4(pack2(v[8 * j], v[8 * j + 1], kHalf), pack2(v[8 * j + 2], v[8 * j + 3], kHalf),
+                          pack2(v[8 * j + 4], v[8 * j + 5], kHalf),
+                          pack2(v[8 * j + 6], v[8 * j + 7], kHalf));
     }
   }
-  if (bad) cache_flag(a.dev_err, ALHR_DEVERR_BLOCK);
 }
 
 template <int D, int CODE, int T>
 cudaError_t store_as(const StoreArgs& a, cudaStream_t st) {
-  const long long units = static_cast<long long>(a.tokens) * a.c.heads * 2;
-  const long long grid = (units + kStoreWarps - 1) / kStoreWarps;
-  store_kernel<D, CODE, T>
-      <<<static_cast<unsigned>(grid < (1 << 20) ? grid : (1 << 20)), kStoreWarps * 32, 0, st>>>(a);
+  // one token a warp while that leaves the GPU room (each may be a run of its own), else 16
+  const long long warps = static_cast<long long>(a.tokens) * a.c.heads * 2;
+  const int per = warps <= 16384 ? 1 : 16;
+  const dim3 grid(static_cast<unsigned>((a.tokens + per - 1) / per),
+                  static_cast<unsigned>((2 * a.c.heads + kStoreWarps - 1) / kStoreWarps));
+  if (grid.y > 65535u) return cudaErrorInvalidConfiguration;
+  store_kernel<D, CODE, T><<<grid, kStoreWarps * 32, 0, st>>>(a, per);
   return cudaGetLastError();
 }
 
 template <int D, int CODE, int T>
 cudaError_t load_as(const LoadArgs& a, cudaStream_t st) {
-  const long long units = static_cast<long long>(a.tokens) * a.c.heads * 2 * (D / 8);
-  const long long grid = (units + 255) / 256;
-  load_kernel<D, CODE, T>
-      <<<static_cast<unsigned>(grid < (1 << 20) ? grid : (1 << 20)), 256, 0, st>>>(a);
+  const int pieces = 2 * a.c.heads * (D / 16);
+  unsigned x = 32;
+  while (x < 256 && x < static_cast<unsigned>(pieces)) x *= 2;
+  const dim3 threads(x, 256 / x);
+  const unsigned grid = (static_cast<unsigned>(a.tokens) + threads.y - 1) / threads.y;
+  load_kernel<D, CODE, T><<<grid, threads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
