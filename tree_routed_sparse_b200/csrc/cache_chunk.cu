@@ -34,6 +34,9 @@ constexpr int kKeys = 128;       // keys of a tile
 constexpr int kChunkThreads = 512;  // warps 0-3, 4-7: rows; 8-11: keys and values; 12: products
 constexpr uint32_t kWaits = 1u << 24;
 constexpr float kTopLog = 7.f;   // log2 of the largest weight when M is set
+// Registers of a thread of the rows', the codes' and the products' warps: 2 * 152 + 120 + 88 =
+// 4 * 128, what the block is launched with.
+constexpr int kRowRegs = 152, kCodeRegs = 120, kProductRegs = 88;
 
 template <int D>
 struct ChunkSmem {
@@ -147,6 +150,35 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+
+// Two fp32 numbers an instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpair(uint64_t d, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(lo), "=f"(hi) : "l"(d));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+template <int REGS>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS));
 }
 
 // One request of the list: more than row_limit rows; groups of kRows rows, each with the key tiles
@@ -283,6 +315,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
   if (warp < 8) {
     // ================ rows: thread (i, lane of the tile) holds one query row
+    more_registers<kRowRegs>();
     const int i = warp >> 2, rt = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lanes + i * 128, o_col = tmem + lanes + 256 + i * D;
@@ -294,7 +327,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       row = cur.group * kRows + i * 128 + rt;
       m = -INFINITY;
       l = 0.f;
-      see = 0;
+      see = 0x7fffffff;  // a row behind the last one masks nothing and is not written
       float top = 0.f;
       const bool on = row < cur.q.rows;
       const uint4* p = nullptr;
@@ -358,72 +391,116 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int seen = see - cur.tile * kKeys;  // columns < seen are visible
         const bool cut = __any_sync(0xffffffffu, seen < kKeys);
         const float4* sc = reinterpret_cast<const float4*>(scales) + b * 8;
-        // the largest x of the row
-        float top = -INFINITY;
+        // Nearly always M stays as it is: weights are taken with it at once, and held until it is
+        // known that none is above 2^15. The tile in which M has to grow, the first one of a unit
+        // and those that a mask cuts take two passes over the scores.
+        bool done = false;
+        if (!first && !cut) {
+          uint32_t p[64];
+          float sum = l, most = m == -INFINITY ? INFINITY : 0.f;
+          uint32_t v[2][32];
+          tmem_ld32(v[0], s_col);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          tmem_ld32(v, s_col + c * 32);
-          wait_ld();
-          if (cut) {
+          for (int c = 0; c < 4; ++c) {
+            wait_ld();
+            if (c < 3) tmem_ld32(v[(c + 1) & 1], s_col + (c + 1) * 32);
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (c * 32 + k >= seen) v[k] = 0xff800000u;  // -infinity
+            for (int u = 0; u < 2; ++u) {
+              const float4 f = sc[c * 2 + u];
+              const float f1 = qs * f.x, f0 = f.y - m;
+              const uint64_t f11 = pair(f1, f1), f00 = pair(f0, f0);
+              uint64_t part = 0;
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                const uint32_t* w = &v[c & 1][u * 16 + k];
+                float x0, x1;
+                unpair(fma2(pair(__uint_as_float(w[0]), __uint_as_float(w[1])), f11, f00), x0, x1);
+                x0 = exp2_fast(x0);
+                x1 = exp2_fast(x1);
+                part = add2(part, pair(x0, x1));
+                p[c * 16 + u * 8 + k / 2] = pack2(x0, x1, true);
+              }
+              float lo, hi;
+              unpair(part, lo, hi);
+              lo += hi;
+              most = fmaxf(most, lo);
+              sum = fmaf(lo, f.z, sum);
+            }
           }
+          done = __all_sync(0xffffffffu, most <= 32768.f);
+          if (done) {
+            l = sum;
+            uint32_t half[32];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            float x = __uint_as_float(v[u * 16]);
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int k = 1; k < 16; ++k) x = fmaxf(x, __uint_as_float(v[u * 16 + k]));
-            const float4 f = sc[c * 2 + u];
-            // -infinity stays where the factor is 0
-            top = fmaxf(top, x == -INFINITY ? x : fmaf(x, qs * f.x, f.y));
-          }
-        }
-        const bool grow = top > m + kTopLog + 8.f;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float mn = fmaxf(m, top - kTopLog);
-          const float keep = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
-          m = mn;
-          l *= keep;
-          if (!first) {
-            // the product before this tile's scores is complete: they were issued after it
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t v[32];
-              tmem_ld32(v, o_col + c * 32);
-              wait_ld();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * keep);
-              tmem_st32(o_col + c * 32, v);
+              for (int k = 0; k < 32; ++k) half[k] = p[h * 32 + k];
+              tmem_st32(s_col + h * 32, half);
             }
           }
         }
-        const float base = m == -INFINITY ? 0.f : m;
+        if (!done) {
+          float top = -INFINITY;  // the largest x of the row
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            tmem_ld32(v, s_col + c * 32);
+            wait_ld();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32], p[16];
-          tmem_ld32(v, s_col + c * 32);
-          wait_ld();
+            for (int u = 0; u < 2; ++u) {
+              float x = -INFINITY;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float4 f = sc[c * 2 + u];
-            const float f1 = qs * f.x, f0 = f.y - base;
-            float part = 0.f;
+              for (int k = 0; k < 16; ++k)
+                if (c * 32 + u * 16 + k < seen) x = fmaxf(x, __uint_as_float(v[u * 16 + k]));
+              const float4 f = sc[c * 2 + u];
+              // -infinity stays where the factor is 0
+              top = fmaxf(top, x == -INFINITY ? x : fmaf(x, qs * f.x, f.y));
+            }
+          }
+          const bool grow = top > m + kTopLog + 8.f;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mn = fmaxf(m, top - kTopLog);
+            const float keep = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
+            m = mn;
+            l *= keep;
+            if (!first) {
+              // the product before this tile's scores is complete: they were issued after it
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t v[32];
+                tmem_ld32(v, o_col + c * 32);
+                wait_ld();
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              float x0 = exp2_fast(fmaf(__uint_as_float(v[u * 16 + k]), f1, f0));
-              float x1 = exp2_fast(fmaf(__uint_as_float(v[u * 16 + k + 1]), f1, f0));
-              if (cut) {
+                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * keep);
+                tmem_st32(o_col + c * 32, v);
+              }
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32], p[16];
+            tmem_ld32(v, s_col + c * 32);
+            wait_ld();
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const float4 f = sc[c * 2 + u];
+              const float f1 = qs * f.x, f0 = f.y - base;
+              float part = 0.f;
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                float x0 = exp2_fast(fmaf(__uint_as_float(v[u * 16 + k]), f1, f0));
+                float x1 = exp2_fast(fmaf(__uint_as_float(v[u * 16 + k + 1]), f1, f0));
                 if (c * 32 + u * 16 + k >= seen) x0 = 0.f;
                 if (c * 32 + u * 16 + k + 1 >= seen) x1 = 0.f;
+                part += x0 + x1;
+                p[u * 8 + k / 2] = pack2(x0, x1, true);
               }
-              part += x0 + x1;
-              p[u * 8 + k / 2] = pack2(x0, x1, true);
+              l = fmaf(part, f.z, l);
             }
-            l = fmaf(part, f.z, l);
+            // over scores that have been read
+            tmem_st16(s_col + c * 16, p);
           }
-          tmem_st16(s_col + c * 16, p);
         }
         wait_st();
         fence_before();
@@ -505,6 +582,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
   } else if (warp < 12) {
     // ================ keys and values: codes to halves
+    fewer_registers<kCodeRegs>();
     const int w = warp - 8;
     const int kr = lane & 7, kc = lane >> 3;       // row of eight, 16-byte piece of 64
     constexpr int kHalves = D / 64;                // pieces kc, kc + 4
@@ -528,15 +606,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     auto fetch = [&](const uint8_t* codes, const ChunkCursor& c, const int (&blk)[2],
                      uint4 (&raw)[4 * kHalves]) {
 #pragma unroll
-      for (int rg = 0; rg < 4; ++rg) {
-        const int key = c.tile * kKeys + w * 32 + rg * 8 + kr;
-        const int block = blk[rg >> 1];
-        const bool on = block >= 0 && key < c.q.see;
-        const long long row = block_row(a.c, max(block, 0), c.h) + (key & (a.c.bs - 1));
-        const uint4* p = reinterpret_cast<const uint4*>(codes + row * D + kc * 16);
+      for (int u = 0; u < 2; ++u) {
+        const int key = c.tile * kKeys + w * 32 + u * 16;
+        const long long row = block_row(a.c, max(blk[u], 0), c.h) + (key & (a.c.bs - 1)) + kr;
+        const uint8_t* p = codes + row * D + kc * 16;
+        const int left = blk[u] < 0 ? 0 : c.q.see - key - kr;  // this lane's rows 0 and 8 are there
 #pragma unroll
-        for (int hh = 0; hh < kHalves; ++hh)
-          raw[rg * kHalves + hh] = on ? __ldg(p + hh * 4) : make_uint4(0u, 0u, 0u, 0u);
+        for (int rg = 0; rg < 2; ++rg)
+#pragma unroll
+          for (int hh = 0; hh < kHalves; ++hh)
+            raw[(u * 2 + rg) * kHalves + hh] =
+                left > rg * 8 ? __ldg(reinterpret_cast<const uint4*>(p + rg * 8 * D + hh * 64))
+                              : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    // lanes 0, 1: scales of this warp's two groups
+    float ks = 0.f, vs = 0.f;
+    auto fetch_scales = [&](const ChunkCursor& c, const int (&blk)[2]) {
+      const int mine = lane == 0 ? blk[0] : blk[1];
+      ks = vs = 0.f;
+      if (lane < 2 && mine >= 0) {
+        const long long si = static_cast<long long>(mine) * a.c.heads + c.h;
+        ks = __ldg(a.c.k_scale + si);
+        vs = __ldg(a.c.v_scale + si);
       }
     };
     auto widen = [&](uint32_t dst, const uint4 (&raw)[4 * kHalves]) {
@@ -562,23 +654,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint4 raw_k[4 * kHalves], raw_v[4 * kHalves];
     int blk[2], blk_next[2] = {-1, -1};
     blocks_of(next, blk);
+    fetch_scales(next, blk);
     fetch(a.c.k, next, blk, raw_k);
     fetch(a.c.v, next, blk, raw_v);
-    ChunkCursor at = next;
     if (count > 1) {
       next.step(a, row_limit);
       blocks_of(next, blk_next);
     }
     for (int j = 0; j < count; ++j) {
       const int b = j & 1;
-      // lanes 0, 1: scales of this warp's groups
-      float ks = 0.f, vs = 0.f;
       const int mine = lane == 0 ? blk[0] : blk[1];
-      if (lane < 2 && mine >= 0) {
-        const long long si = static_cast<long long>(mine) * a.c.heads + at.h;
-        ks = __ldg(a.c.k_scale + si);
-        vs = __ldg(a.c.v_scale + si);
-      }
       if (j >= 2) {
         if (!warp_wait(bar(kKEmpty, b), ((j >> 1) - 1) & 1, stop)) break;
         if (!warp_wait(bar(kScFree, b), ((j >> 1) - 1) & 1, stop)) break;
@@ -593,7 +678,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       fence_shared();
       __syncwarp();
       if (lane == 0) bar_arrive(bar(kKFull, b));
-      if (j + 1 < count) fetch(a.c.k, next, blk_next, raw_k);
+      if (j + 1 < count) {
+        fetch_scales(next, blk_next);
+        fetch(a.c.k, next, blk_next, raw_k);
+      }
       if (j >= 2 && !warp_wait(bar(kVEmpty, b), ((j >> 1) - 1) & 1, stop)) break;
       widen(smem + L::v + b * L::kTile, raw_v);
       fence_shared();
@@ -603,7 +691,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         fetch(a.c.v, next, blk_next, raw_v);
         blk[0] = blk_next[0];
         blk[1] = blk_next[1];
-        at = next;
         if (j + 2 < count) {
           next.step(a, row_limit);
           blocks_of(next, blk_next);
@@ -611,7 +698,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) cache_flag(a.dev_err, ALHR_DEVERR_BLOCK);
-  } else if (warp == 12 && lane == 0) {
+  } else {
+    fewer_registers<kProductRegs>();
+  }
+  if (warp == 12 && lane == 0) {
     // ================ products
     constexpr uint32_t kRowGroup = kCols * 128;  // bytes between groups of eight rows
     constexpr uint32_t kScore = product_desc(128, false), kSum = product_desc(D, true);
