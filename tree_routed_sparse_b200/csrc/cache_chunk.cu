@@ -109,6 +109,13 @@ __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, u
       "r"(a), "l"(b), "r"(idesc), "r"(add)
       : "memory");
 }
+// True in one lane of a warp that is together; the compiler knows what it guards to be uniform.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n"
+               : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void commit_to(uint32_t bar) {
   asm volatile(
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar)
@@ -209,39 +216,44 @@ struct ChunkRequest {
 struct ChunkCursor {
   ChunkRequest q;
   int r, h, group, tile, tiles;
-  // false when the next tile belongs to another unit
-  __device__ __forceinline__ void step(const AttendArgs& a, int row_limit) {
-    if (++tile < tiles) return;
-    tile = 0;
-    if (++group == q.groups) {
-      group = 0;
-      if (++h == a.c.heads) {
-        h = 0;
-        do {
-          if (++r >= a.requests) {  // not reached: the list has ended before
-            r = a.requests - 1;
-            q.groups = 1;
-            break;
-          }
-          q.load(a, r, row_limit);
-        } while (q.groups == 0);
-      }
-    }
-    tiles = q.tiles(a, group);
-  }
   __device__ __forceinline__ int rows_here() const { return min(kRows, q.rows - group * kRows); }
 };
 
+// The unit behind c's.
+__device__ __forceinline__ ChunkCursor next_unit(const AttendArgs* a, ChunkCursor c, int row_limit) {
+  c.tile = 0;
+  if (++c.group == c.q.groups) {
+    c.group = 0;
+    if (++c.h == a->c.heads) {
+      c.h = 0;
+      do {
+        if (++c.r >= a->requests) {  // not reached: the list has ended before
+          c.r = a->requests - 1;
+          c.q.groups = 1;
+          break;
+        }
+        c.q.load(*a, c.r, row_limit);
+      } while (c.q.groups == 0);
+    }
+  }
+  c.tiles = c.q.tiles(*a, c.group);
+  return c;
+}
+#define ALHR_STEP(c) \
+  do { if (++(c).tile >= (c).tiles) (c) = next_unit(&a, (c), row_limit); } while (0)
+
 template <int D, int CODE>
 __global__ void __launch_bounds__(kChunkThreads, 1)
-    chunk_kernel(const AttendArgs a, const JoinSpace space, const int row_limit) {
+    chunk_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ JoinSpace space,
+                 const int row_limit) {
   using L = ChunkSmem<D>;
   constexpr int kCols = D / 8;  // 16-byte columns of a row of halves
   extern __shared__ __align__(1024) unsigned char chunk_smem[];
   __shared__ long long chunk_start[kChunkThreads];
   __shared__ long long warp_sum[kChunkThreads / 32];
   const uint32_t smem = shared_u32(chunk_smem);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t bars = smem + L::bars;
   auto bar = [&](int which, int i = 0) { return bars + (which + i) * 8; };
   volatile int* stop = reinterpret_cast<volatile int*>(chunk_smem + L::misc);
@@ -338,6 +350,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         p = reinterpret_cast<const uint4*>(
             static_cast<const uint16_t*>(a.q) + (cur.q.q_lo + tok) * a.q_token_stride +
             (cur.h * a.group + (row - tok * a.group)) * a.q_head_stride);
+#pragma unroll 4
         for (int c = 0; c < kCols; ++c) {
           const uint4 w = __ldg(p + c);
           float y[8];
@@ -354,6 +367,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                                  a.scale_log2);
       qs = __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23) * fabsf(a.scale_log2);
       const uint32_t dst = smem + L::q + i * L::kTile + (rt >> 3) * (kCols * 128) + (rt & 7) * 16;
+#pragma unroll 2
       for (int c = 0; c < kCols; ++c) {
         uint4 w = make_uint4(0u, 0u, 0u, 0u);
         if (on) {
@@ -372,15 +386,84 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       __syncwarp();
       if (lane == 0) bar_arrive(bar(kQFull, i));
     };
-    bool first = true, from_start = cur.tile == 0;
+    bool first = true, fresh = true, from_start = cur.tile == 0, busy = false;
     int units = 0;
-    bool busy = cur.rows_here() > i * 128;  // the second tile of rows may be empty
-    if (busy) load_q();
     uint32_t s_phase = 0;
-    for (int j = 0; j < count; ++j) {
+    for (int j = 0;; ++j) {
+      if (fresh) {
+        // ---- the unit before (or this piece of it) has ended, another one begins
+        const ChunkCursor was = cur;
+        const int was_row = row;
+        const float was_m = m, was_l = l;
+        const bool was_busy = busy, to_end = cur.tile + 1 == cur.tiles, started = from_start;
+        first = true;
+        fresh = false;
+        if (j > 0 && j < count) {
+          ALHR_STEP(cur);
+          from_start = true;
+        }
+        if (j < count) {
+          busy = cur.rows_here() > i * 128;  // the second tile of rows may be empty
+          // S of the last tile is here, so nothing reads the queries before any more
+          if (busy) load_q();
+        }
+        if (j > 0 && tid == 0 && started && !to_end) {
+          meta->r = was.r;
+          meta->h = was.h;
+          meta->row0 = was.group * kRows;
+          meta->rows = was.rows_here();
+          meta->last = split.piece_of(end - 1 + (was.tiles - 1 - was.tile));
+        }
+        if (j > 0 && was_busy) {
+          if (!warp_wait(bar(kODone, i), units & 1, stop)) break;
+          ++units;
+          fence_after();
+          const bool on = was_row < was.q.rows, whole = started && to_end;
+          const int tok = was_row / a.group;
+          const long long at = static_cast<long long>(was.q.q_lo + tok) * a.q_heads +
+                               was.h * a.group + (was_row - tok * a.group);
+          const float inv = was_l > 0.f ? 1.f / was_l : 0.f;
+          float* part = space.part + (static_cast<long long>(piece) * 2 + (started ? 1 : 0)) *
+                                         (kRows * (D + 2));
+          const int pr = i * 128 + rt;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            __syncwarp();
+            tmem_ld32(v, o_col + c * 32);
+            wait_ld();
+            if (on && whole) {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D + c * 32);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  w[e] = pack2(__uint_as_float(v[k * 8 + 2 * e]) * inv,
+                               __uint_as_float(v[k * 8 + 2 * e + 1]) * inv, a.fp16);
+                dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else if (on) {
+              uint4* dst = reinterpret_cast<uint4*>(part + pr * D + c * 32);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            }
+          }
+          if (on && whole) {
+            if (a.lse)
+              a.lse[at] = was_l > 0.f ? (was_m + log2f(was_l)) * 0.6931471805599453f : -INFINITY;
+          } else if (on) {
+            part[kRows * D + pr] = was_m;
+            part[kRows * D + kRows + pr] = was_l;
+          }
+          __syncwarp();
+          fence_before();
+        }
+      }
+      if (j == count) break;
       const int b = j & 1;
       if (!warp_wait(bar(kKFull, b), (j >> 1) & 1, stop)) break;
-      const bool last = cur.tile + 1 == cur.tiles || j + 1 == count;
       if (!busy) {
         __syncwarp();
         if (lane == 0) bar_arrive(bar(kScFree, b));
@@ -396,47 +479,47 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         // and those that a mask cuts take two passes over the scores.
         bool done = false;
         if (!first && !cut) {
-          uint32_t p[64];
+          uint32_t kept[32], p[32];  // weights of columns 0-63, 64-127
           float sum = l, most = m == -INFINITY ? INFINITY : 0.f;
-          uint32_t v[2][32];
-          tmem_ld32(v[0], s_col);
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            wait_ld();
-            if (c < 3) tmem_ld32(v[(c + 1) & 1], s_col + (c + 1) * 32);
+            for (int k = 0; k < 32; ++k) kept[k] = p[k];
+            uint32_t v[2][32];
+            tmem_ld32(v[0], s_col + h * 64);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const float4 f = sc[c * 2 + u];
-              const float f1 = qs * f.x, f0 = f.y - m;
-              const uint64_t f11 = pair(f1, f1), f00 = pair(f0, f0);
-              uint64_t part = 0;
+            for (int c = 0; c < 2; ++c) {
+              wait_ld();
+              if (c == 0) tmem_ld32(v[1], s_col + h * 64 + 32);
 #pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                const uint32_t* w = &v[c & 1][u * 16 + k];
-                float x0, x1;
-                unpair(fma2(pair(__uint_as_float(w[0]), __uint_as_float(w[1])), f11, f00), x0, x1);
-                x0 = exp2_fast(x0);
-                x1 = exp2_fast(x1);
-                part = add2(part, pair(x0, x1));
-                p[c * 16 + u * 8 + k / 2] = pack2(x0, x1, true);
+              for (int u = 0; u < 2; ++u) {
+                const float4 f = sc[h * 4 + c * 2 + u];
+                const float f1 = qs * f.x, f0 = f.y - m;
+                const uint64_t f11 = pair(f1, f1), f00 = pair(f0, f0);
+                uint64_t part = 0;
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                  const uint32_t* w = &v[c][u * 16 + k];
+                  float x0, x1;
+                  unpair(fma2(pair(__uint_as_float(w[0]), __uint_as_float(w[1])), f11, f00), x0, x1);
+                  x0 = exp2_fast(x0);
+                  x1 = exp2_fast(x1);
+                  part = add2(part, pair(x0, x1));
+                  p[c * 16 + u * 8 + k / 2] = pack2(x0, x1, true);
+                }
+                float lo, hi;
+                unpair(part, lo, hi);
+                lo += hi;
+                most = fmaxf(most, lo);
+                sum = fmaf(lo, f.z, sum);
               }
-              float lo, hi;
-              unpair(part, lo, hi);
-              lo += hi;
-              most = fmaxf(most, lo);
-              sum = fmaf(lo, f.z, sum);
             }
           }
           done = __all_sync(0xffffffffu, most <= 32768.f);
           if (done) {
             l = sum;
-            uint32_t half[32];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) half[k] = p[h * 32 + k];
-              tmem_st32(s_col + h * 32, half);
-            }
+            tmem_st32(s_col, kept);
+            tmem_st32(s_col + 32, p);
           }
         }
         if (!done) {
@@ -511,74 +594,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
       }
       first = false;
-      if (!last) {
-        ++cur.tile;
-        continue;
-      }
-      // ---- the unit (or this piece of it) ends
-      const ChunkCursor was = cur;
-      const int was_row = row;
-      const float was_m = m, was_l = l;
-      const bool was_busy = busy, to_end = cur.tile + 1 == cur.tiles, started = from_start;
-      first = from_start = true;
-      if (j + 1 < count) {
-        cur.step(a, row_limit);
-        busy = cur.rows_here() > i * 128;
-        // S of the last tile is here, so nothing reads this tile of queries any more
-        if (busy) load_q();
-      }
-      if (was_busy) {
-        if (!warp_wait(bar(kODone, i), units & 1, stop)) break;
-        ++units;
-        fence_after();
-        const bool on = was_row < was.q.rows;
-        const int tok = was_row / a.group;
-        const long long at = static_cast<long long>(was.q.q_lo + tok) * a.q_heads +
-                             was.h * a.group + (was_row - tok * a.group);
-        const float inv = was_l > 0.f ? 1.f / was_l : 0.f;
-        float* part = space.part + (static_cast<long long>(piece) * 2 + (started ? 1 : 0)) *
-                                       (kRows * (D + 2));
-        const int pr = i * 128 + rt;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t v[32];
-          tmem_ld32(v, o_col + c * 32);
-          wait_ld();
-          if (on && started && to_end) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D + c * 32);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack2(__uint_as_float(v[k * 8 + 2 * e]) * inv,
-                             __uint_as_float(v[k * 8 + 2 * e + 1]) * inv, a.fp16);
-              dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          } else if (on) {
-            uint4* dst = reinterpret_cast<uint4*>(part + pr * D + c * 32);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-          }
-          __syncwarp();
-        }
-        if (on && started && to_end) {
-          if (a.lse)
-            a.lse[at] = was_l > 0.f ? (was_m + log2f(was_l)) * 0.6931471805599453f : -INFINITY;
-        } else if (on) {
-          part[kRows * D + pr] = was_m;
-          part[kRows * D + kRows + pr] = was_l;
-        }
-        fence_before();
-      }
-      if (tid == 0 && started && !to_end) {
-        meta->r = was.r;
-        meta->h = was.h;
-        meta->row0 = was.group * kRows;
-        meta->rows = was.rows_here();
-        meta->last = split.piece_of(end - 1 + (was.tiles - 1 - was.tile));
-      }
+      fresh = cur.tile + 1 == cur.tiles || j + 1 == count;
+      if (!fresh) ++cur.tile;
     }
   } else if (warp < 12) {
     // ================ keys and values: codes to halves
@@ -652,47 +669,43 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
     };
     uint4 raw_k[4 * kHalves], raw_v[4 * kHalves];
-    int blk[2], blk_next[2] = {-1, -1};
-    blocks_of(next, blk);
-    fetch_scales(next, blk);
-    fetch(a.c.k, next, blk, raw_k);
-    fetch(a.c.v, next, blk, raw_v);
-    if (count > 1) {
-      next.step(a, row_limit);
-      blocks_of(next, blk_next);
-    }
-    for (int j = 0; j < count; ++j) {
+    int blk[2] = {-1, -1}, blk_next[2];
+    blocks_of(next, blk_next);
+    for (int j = -1; j < count; ++j) {  // tile j is widened, tile j + 1 asked for
       const int b = j & 1;
-      const int mine = lane == 0 ? blk[0] : blk[1];
-      if (j >= 2) {
-        if (!warp_wait(bar(kKEmpty, b), ((j >> 1) - 1) & 1, stop)) break;
-        if (!warp_wait(bar(kScFree, b), ((j >> 1) - 1) & 1, stop)) break;
+      if (j >= 0) {
+        if (j >= 2) {
+          if (!warp_wait(bar(kKEmpty, b), ((j >> 1) - 1) & 1, stop)) break;
+          if (!warp_wait(bar(kScFree, b), ((j >> 1) - 1) & 1, stop)) break;
+        }
+        widen(smem + L::k + b * L::kTile, raw_k);
+        if (lane < 2) {
+          const float v1 = fmaxf(vs, kTinyScale);
+          float4 f = make_float4(ks, __log2f(v1), __frcp_rn(v1), 0.f);
+          if ((lane == 0 ? blk[0] : blk[1]) < 0) f = make_float4(0.f, -INFINITY, 0.f, 0.f);
+          reinterpret_cast<float4*>(chunk_smem + L::scales)[b * 8 + w * 2 + lane] = f;
+        }
+        fence_shared();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar(kKFull, b));
       }
-      widen(smem + L::k + b * L::kTile, raw_k);
-      if (lane < 2) {
-        const float v1 = fmaxf(vs, kTinyScale);
-        float4 f = make_float4(ks, __log2f(v1), __frcp_rn(v1), 0.f);
-        if (mine < 0) f = make_float4(0.f, -INFINITY, 0.f, 0.f);
-        reinterpret_cast<float4*>(chunk_smem + L::scales)[b * 8 + w * 2 + lane] = f;
-      }
-      fence_shared();
-      __syncwarp();
-      if (lane == 0) bar_arrive(bar(kKFull, b));
       if (j + 1 < count) {
         fetch_scales(next, blk_next);
         fetch(a.c.k, next, blk_next, raw_k);
       }
-      if (j >= 2 && !warp_wait(bar(kVEmpty, b), ((j >> 1) - 1) & 1, stop)) break;
-      widen(smem + L::v + b * L::kTile, raw_v);
-      fence_shared();
-      __syncwarp();
-      if (lane == 0) bar_arrive(bar(kVFull, b));
+      if (j >= 0) {
+        if (j >= 2 && !warp_wait(bar(kVEmpty, b), ((j >> 1) - 1) & 1, stop)) break;
+        widen(smem + L::v + b * L::kTile, raw_v);
+        fence_shared();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar(kVFull, b));
+      }
       if (j + 1 < count) {
         fetch(a.c.v, next, blk_next, raw_v);
         blk[0] = blk_next[0];
         blk[1] = blk_next[1];
         if (j + 2 < count) {
-          next.step(a, row_limit);
+          ALHR_STEP(next);
           blocks_of(next, blk_next);
         }
       }
@@ -701,61 +714,65 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   } else {
     fewer_registers<kProductRegs>();
   }
-  if (warp == 12 && lane == 0) {
-    // ================ products
+  if (warp == 12) {
+    // ================ products: the warp waits together, one lane asks for them
     constexpr uint32_t kRowGroup = kCols * 128;  // bytes between groups of eight rows
     constexpr uint32_t kScore = product_desc(128, false), kSum = product_desc(D, true);
-    auto scores = [&](int i, int b) {
-      const uint32_t qa = smem + L::q + i * L::kTile, ka = smem + L::k + b * L::kTile;
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s)
-        product_ss(tmem + i * 128, operand_desc(qa + s * 256, 128, kRowGroup),
-                   operand_desc(ka + s * 256, 128, kRowGroup), kScore, s > 0);
-    };
-    auto sums = [&](int i, int b, bool add) {
-      const uint32_t va = smem + L::v + b * L::kTile;
-#pragma unroll
-      for (int s = 0; s < kKeys / 16; ++s)
-        product_ts(tmem + 256 + i * D, tmem + i * 128 + s * 8,
-                   operand_desc(va + s * 2 * kRowGroup, kRowGroup, 128), kSum, add || s > 0);
-    };
-    bool ok = true;
-    uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-    // tile j's scores for both tiles of rows are asked for while tile j - 1 is summed
+    uint32_t phases = 0;  // bit i: of Q of tile i of rows, bit 2 + i: of its weights
     int subs = cur.rows_here() > 128 ? 2 : 1;
+    // scores of tile j for tile i of rows
     auto ask = [&](int i, int j, bool fresh) {
       if (fresh) {
-        if (!bar_wait(bar(kQFull, i), q_phase[i], stop)) return false;
-        q_phase[i] ^= 1u;
+        if (!warp_wait(bar(kQFull, i), (phases >> i) & 1u, stop)) return false;
+        phases ^= 1u << i;
       }
-      if (!bar_wait(bar(kKFull, j & 1), (j >> 1) & 1, stop)) return false;
+      if (!warp_wait(bar(kKFull, j & 1), (j >> 1) & 1, stop)) return false;
       fence_after();
-      scores(i, j & 1);
-      commit_to(bar(kSFull, i));
+      const uint64_t q = operand_desc(smem + L::q + i * L::kTile, 128, kRowGroup);
+      const uint64_t k = operand_desc(smem + L::k + (j & 1) * L::kTile, 128, kRowGroup);
+      if (elected()) {
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+          product_ss(tmem + i * 128, q + s * 16, k + s * 16, kScore, s > 0);
+        commit_to(bar(kSFull, i));
+      }
+      __syncwarp();
       return true;
     };
-    for (int i = 0; i < subs && ok; ++i) ok = ask(i, 0, true);
-    if (ok) commit_to(bar(kKEmpty, 0));
-    bool add = false;
-    for (int j = 0; j < count && ok; ++j) {
-      const bool last = cur.tile + 1 == cur.tiles || j + 1 == count;
+    // Step j sums tile j and asks for the scores of tile j + 1 (step -1: of tile 0 alone), so that
+    // one tile of rows takes its weights while the products of the other one run.
+    bool ok = true, add = false;
+#pragma unroll 1
+    for (int j = -1; j < count && ok; ++j) {
+      const bool last = j < 0 || cur.tile + 1 == cur.tiles;
       ChunkCursor after = cur;
-      if (j + 1 < count) after.step(a, row_limit);
+      if (j >= 0 && j + 1 < count) ALHR_STEP(after);
       const int subs_after = after.rows_here() > 128 ? 2 : 1;
+#pragma unroll 1
       for (int i = 0; i < 2 && ok; ++i) {
-        if (i < subs) {
-          ok = bar_wait(bar(kPFull, i), p_phase[i], stop);
-          p_phase[i] ^= 1u;
-          if (ok && i == 0) ok = bar_wait(bar(kVFull, j & 1), (j >> 1) & 1, stop);
+        if (j >= 0 && i < subs) {
+          ok = warp_wait(bar(kPFull, i), (phases >> (2 + i)) & 1u, stop);
+          phases ^= 4u << i;
+          if (ok && i == 0) ok = warp_wait(bar(kVFull, j & 1), (j >> 1) & 1, stop);
           if (!ok) break;
           fence_after();
-          sums(i, j & 1, add);
-          if (last) commit_to(bar(kODone, i));
+          const uint64_t v = operand_desc(smem + L::v + (j & 1) * L::kTile, kRowGroup, 128);
+          if (elected()) {
+#pragma unroll
+            for (int s = 0; s < kKeys / 16; ++s)
+              product_ts(tmem + 256 + i * D, tmem + i * 128 + s * 8, v + s * (2 * kRowGroup / 16),
+                         kSum, add || s > 0);
+            if (last || j + 1 == count) commit_to(bar(kODone, i));
+            if (i == subs - 1) commit_to(bar(kVEmpty, j & 1));
+          }
+          __syncwarp();
         }
-        if (i == subs - 1) commit_to(bar(kVEmpty, j & 1));
         if (j + 1 < count && i < subs_after) {
           ok = ask(i, j + 1, last);
-          if (ok && i == subs_after - 1) commit_to(bar(kKEmpty, (j + 1) & 1));
+          if (ok && i == subs_after - 1) {
+            if (elected()) commit_to(bar(kKEmpty, (j + 1) & 1));
+            __syncwarp();
+          }
         }
       }
       add = !last;
@@ -763,9 +780,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       subs = subs_after;
     }
     if (!ok) {  // products in flight end before the tensor memory is freed
-      commit_to(bar(kDrain));
+      if (elected()) commit_to(bar(kDrain));
+      __syncwarp();
       *stop = 0;
-      bar_wait(bar(kDrain), 0, stop);
+      warp_wait(bar(kDrain), 0, stop);
       *stop = 1;
     }
   }
