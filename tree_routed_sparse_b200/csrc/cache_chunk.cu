@@ -9,7 +9,7 @@
 // 128. Four warps load codes to registers, widen them to halves (exact) and write them to shared
 // memory in the core-matrix layout of tcgen05 (8 rows of 16 bytes): for the keys (rows of the
 // second operand) K-major, and the same bytes read MN-major are the values' operand, so nothing is
-// transposed. One thread issues the products: S_i = Q_i K^T into tensor memory, and O_i += P_i V
+// transposed. Two warps ask for the products: S_i = Q_i K^T into tensor memory, and O_i += P_i V
 // with P_i read from tensor memory, where the rows' threads put it in place of S_i. While the
 // tensor core works on one tile of rows the threads of the other one take their powers of two.
 // Rows of a request are (token, head of the group) pairs, so that grouped heads share every key
@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kRows = 256;       // query rows of a unit: two tiles of 128
 constexpr int kKeys = 128;       // keys of a tile
-constexpr int kChunkThreads = 512;  // warps 0-3, 4-7: rows; 8-11: keys and values; 12: products
+constexpr int kChunkThreads = 512;  // warps 0-3, 4-7: rows; 8-11: keys and values; 12, 13: products
 constexpr uint32_t kWaits = 1u << 24;
 constexpr float kTopLog = 7.f;   // log2 of the largest weight when M is set
 // Registers of a thread of the rows', the codes' and the products' warps: 2 * 152 + 120 + 88 =
@@ -51,7 +51,7 @@ struct ChunkSmem {
 };
 
 enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kScFree = 8, kSFull = 10, kPFull = 12,
-           kQFull = 14, kODone = 16, kDrain = 18, kBars = 19 };
+           kQFull = 14, kODone = 16, kDrain = 18 };
 
 __device__ __forceinline__ void bar_init(uint32_t bar, int count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
@@ -219,28 +219,32 @@ struct ChunkCursor {
   __device__ __forceinline__ int rows_here() const { return min(kRows, q.rows - group * kRows); }
 };
 
-// The unit behind c's.
-__device__ __forceinline__ ChunkCursor next_unit(const AttendArgs* a, ChunkCursor c, int row_limit) {
+// The unit behind *c's, where c is the calling warp's own cursor in shared memory (it is looked at
+// when a unit ends only, and registers are short).
+__device__ __forceinline__ ChunkCursor next_unit(const AttendArgs& a, ChunkCursor* cursor,
+                                                 int row_limit) {
+  ChunkCursor c = *cursor;
   c.tile = 0;
   if (++c.group == c.q.groups) {
     c.group = 0;
-    if (++c.h == a->c.heads) {
+    if (++c.h == a.c.heads) {
       c.h = 0;
       do {
-        if (++c.r >= a->requests) {  // not reached: the list has ended before
-          c.r = a->requests - 1;
+        if (++c.r >= a.requests) {  // not reached: the list has ended before
+          c.r = a.requests - 1;
           c.q.groups = 1;
           break;
         }
-        c.q.load(*a, c.r, row_limit);
+        c.q.load(a, c.r, row_limit);
       } while (c.q.groups == 0);
     }
   }
-  c.tiles = c.q.tiles(*a, c.group);
+  c.tiles = c.q.tiles(a, c.group);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) *cursor = c;
+  __syncwarp();
   return c;
 }
-#define ALHR_STEP(c) \
-  do { if (++(c).tile >= (c).tiles) (c) = next_unit(&a, (c), row_limit); } while (0)
 
 template <int D, int CODE>
 __global__ void __launch_bounds__(kChunkThreads, 1)
@@ -251,6 +255,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   extern __shared__ __align__(1024) unsigned char chunk_smem[];
   __shared__ long long chunk_start[kChunkThreads];
   __shared__ long long warp_sum[kChunkThreads / 32];
+  __shared__ ChunkCursor cursors[kChunkThreads / 32];
   const uint32_t smem = shared_u32(chunk_smem);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -296,6 +301,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     cur.tile = static_cast<int>(rest);
   }
   const int count = static_cast<int>(min(end - begin, 0x7fffffffLL));
+  if (lane == 0) cursors[warp] = cur;
+  ChunkCursor* const cursor = &cursors[warp];
 
   if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
@@ -307,16 +314,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       bar_init(bar(kKFull, i), 4);
-      bar_init(bar(kKEmpty, i), 1);
+      bar_init(bar(kKEmpty, i), 2);
       bar_init(bar(kVFull, i), 4);
-      bar_init(bar(kVEmpty, i), 1);
+      bar_init(bar(kVEmpty, i), 2);
       bar_init(bar(kScFree, i), 8);
       bar_init(bar(kSFull, i), 1);
       bar_init(bar(kPFull, i), 4);
       bar_init(bar(kQFull, i), 4);
       bar_init(bar(kODone, i), 1);
+      bar_init(bar(kDrain, i), 1);
     }
-    bar_init(bar(kDrain), 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     *stop = 0;
   }
@@ -333,20 +340,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint32_t s_col = tmem + lanes + i * 128, o_col = tmem + lanes + 256 + i * D;
     const unsigned char* scales = chunk_smem + L::scales;
     float m = -INFINITY, l = 0.f, qs = 0.f;
-    int see = 0, row = 0;
+    int seen = 0, row = 0;  // columns < seen of the tile are visible
     // this row's queries to shared memory, scaled by a power of two so that halves hold them
-    auto load_q = [&]() {
+    auto load_q = [&](const ChunkCursor& cur) {
       row = cur.group * kRows + i * 128 + rt;
       m = -INFINITY;
       l = 0.f;
-      see = 0x7fffffff;  // a row behind the last one masks nothing and is not written
+      seen = 0x7fffffff;  // a row behind the last one masks nothing and is not written
       float top = 0.f;
       const bool on = row < cur.q.rows;
       const uint4* p = nullptr;
       if (on) {
         const int tok = row / a.group;
-        see = static_cast<int>(max(min(static_cast<long long>(cur.q.ctx) + tok + 1,
-                                       static_cast<long long>(cur.q.see)), 0LL));
+        seen = static_cast<int>(max(min(static_cast<long long>(cur.q.ctx) + tok + 1,
+                                        static_cast<long long>(cur.q.see)), 0LL));
         p = reinterpret_cast<const uint4*>(
             static_cast<const uint16_t*>(a.q) + (cur.q.q_lo + tok) * a.q_token_stride +
             (cur.h * a.group + (row - tok * a.group)) * a.q_head_stride);
@@ -386,33 +393,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       __syncwarp();
       if (lane == 0) bar_arrive(bar(kQFull, i));
     };
-    bool first = true, fresh = true, from_start = cur.tile == 0, busy = false;
-    int units = 0;
+    bool first = true, fresh = true, from_start = true, busy = false;
+    int units = 0, left = 0;  // key tiles of the unit that are still to come
     uint32_t s_phase = 0;
     for (int j = 0;; ++j) {
       if (fresh) {
         // ---- the unit before (or this piece of it) has ended, another one begins
-        const ChunkCursor was = cur;
+        const ChunkCursor was = *cursor;
         const int was_row = row;
         const float was_m = m, was_l = l;
-        const bool was_busy = busy, to_end = cur.tile + 1 == cur.tiles, started = from_start;
-        first = true;
-        fresh = false;
-        if (j > 0 && j < count) {
-          ALHR_STEP(cur);
-          from_start = true;
-        }
-        if (j < count) {
-          busy = cur.rows_here() > i * 128;  // the second tile of rows may be empty
-          // S of the last tile is here, so nothing reads the queries before any more
-          if (busy) load_q();
-        }
+        const bool was_busy = busy, to_end = left == 0, started = from_start;
         if (j > 0 && tid == 0 && started && !to_end) {
           meta->r = was.r;
           meta->h = was.h;
           meta->row0 = was.group * kRows;
           meta->rows = was.rows_here();
-          meta->last = split.piece_of(end - 1 + (was.tiles - 1 - was.tile));
+          meta->last = split.piece_of(end - 1 + left);
+        }
+        first = true;
+        fresh = false;
+        if (j < count) {
+          ChunkCursor now = was;
+          if (j > 0) now = next_unit(a, cursor, row_limit);
+          from_start = now.tile == 0;
+          left = now.tiles - now.tile;
+          busy = now.rows_here() > i * 128;  // the second tile of rows may be empty
+          // S of the last tile is here, so nothing reads the queries before any more
+          if (busy) load_q(now);
+          seen -= now.tile * kKeys;
         }
         if (j > 0 && was_busy) {
           if (!warp_wait(bar(kODone, i), units & 1, stop)) break;
@@ -471,7 +479,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (!warp_wait(bar(kSFull, i), s_phase, stop)) break;
         s_phase ^= 1u;
         fence_after();
-        const int seen = see - cur.tile * kKeys;  // columns < seen are visible
         const bool cut = __any_sync(0xffffffffu, seen < kKeys);
         const float4* sc = reinterpret_cast<const float4*>(scales) + b * 8;
         // Nearly always M stays as it is: weights are taken with it at once, and held until it is
@@ -594,8 +601,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
       }
       first = false;
-      fresh = cur.tile + 1 == cur.tiles || j + 1 == count;
-      if (!fresh) ++cur.tile;
+      --left;
+      fresh = left == 0 || j + 1 == count;
+      seen -= kKeys;
     }
   } else if (warp < 12) {
     // ================ keys and values: codes to halves
@@ -604,15 +612,28 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int kr = lane & 7, kc = lane >> 3;       // row of eight, 16-byte piece of 64
     constexpr int kHalves = D / 64;                // pieces kc, kc + 4
     bool bad = false;
-    ChunkCursor next = cur;                        // the tile whose codes are asked for
+    // the tile whose codes are asked for
+    int key0 = cur.tile * kKeys + w * 32, key_end = cur.q.see, left = cur.tiles - cur.tile;
+    int head = cur.h;
+    const int32_t* table = a.table + static_cast<long long>(cur.r) * a.max_blocks;
+    auto step = [&]() {
+      key0 += kKeys;
+      if (--left) return;
+      const ChunkCursor c = next_unit(a, cursor, row_limit);
+      key0 = w * 32;
+      key_end = c.q.see;
+      left = c.tiles;
+      head = c.h;
+      table = a.table + static_cast<long long>(c.r) * a.max_blocks;
+    };
     // blocks of the two 16-key groups of this warp's 32 keys
-    auto blocks_of = [&](const ChunkCursor& c, int (&blk)[2]) {
+    auto blocks_of = [&](int (&blk)[2]) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int key = c.tile * kKeys + w * 32 + u * 16;
+        const int key = key0 + u * 16;
         blk[u] = -1;
-        if (key < c.q.see) {
-          blk[u] = __ldg(a.table + static_cast<long long>(c.r) * a.max_blocks + (key >> a.c.bs_log));
+        if (key < key_end) {
+          blk[u] = __ldg(table + (key >> a.c.bs_log));
           if (blk[u] < 0 || blk[u] >= a.c.blocks) {
             blk[u] = -1;
             bad = true;
@@ -620,30 +641,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
       }
     };
-    auto fetch = [&](const uint8_t* codes, const ChunkCursor& c, const int (&blk)[2],
-                     uint4 (&raw)[4 * kHalves]) {
+    auto fetch = [&](const uint8_t* codes, const int (&blk)[2], uint4 (&raw)[4 * kHalves]) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int key = c.tile * kKeys + w * 32 + u * 16;
-        const long long row = block_row(a.c, max(blk[u], 0), c.h) + (key & (a.c.bs - 1)) + kr;
+        const int key = key0 + u * 16;
+        const long long row = block_row(a.c, max(blk[u], 0), head) + (key & (a.c.bs - 1)) + kr;
         const uint8_t* p = codes + row * D + kc * 16;
-        const int left = blk[u] < 0 ? 0 : c.q.see - key - kr;  // this lane's rows 0 and 8 are there
+        const int there = blk[u] < 0 ? 0 : key_end - key - kr;  // this lane's rows 0 and 8
 #pragma unroll
         for (int rg = 0; rg < 2; ++rg)
 #pragma unroll
           for (int hh = 0; hh < kHalves; ++hh)
             raw[(u * 2 + rg) * kHalves + hh] =
-                left > rg * 8 ? __ldg(reinterpret_cast<const uint4*>(p + rg * 8 * D + hh * 64))
+                there > rg * 8 ? __ldg(reinterpret_cast<const uint4*>(p + rg * 8 * D + hh * 64))
                               : make_uint4(0u, 0u, 0u, 0u);
       }
     };
     // lanes 0, 1: scales of this warp's two groups
     float ks = 0.f, vs = 0.f;
-    auto fetch_scales = [&](const ChunkCursor& c, const int (&blk)[2]) {
+    auto fetch_scales = [&](const int (&blk)[2]) {
       const int mine = lane == 0 ? blk[0] : blk[1];
       ks = vs = 0.f;
       if (lane < 2 && mine >= 0) {
-        const long long si = static_cast<long long>(mine) * a.c.heads + c.h;
+        const long long si = static_cast<long long>(mine) * a.c.heads + head;
         ks = __ldg(a.c.k_scale + si);
         vs = __ldg(a.c.v_scale + si);
       }
@@ -670,7 +690,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     };
     uint4 raw_k[4 * kHalves], raw_v[4 * kHalves];
     int blk[2] = {-1, -1}, blk_next[2];
-    blocks_of(next, blk_next);
+    blocks_of(blk_next);
+#pragma unroll 1
     for (int j = -1; j < count; ++j) {  // tile j is widened, tile j + 1 asked for
       const int b = j & 1;
       if (j >= 0) {
@@ -690,8 +711,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (lane == 0) bar_arrive(bar(kKFull, b));
       }
       if (j + 1 < count) {
-        fetch_scales(next, blk_next);
-        fetch(a.c.k, next, blk_next, raw_k);
+        fetch_scales(blk_next);
+        fetch(a.c.k, blk_next, raw_k);
       }
       if (j >= 0) {
         if (j >= 2 && !warp_wait(bar(kVEmpty, b), ((j >> 1) - 1) & 1, stop)) break;
@@ -701,12 +722,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (lane == 0) bar_arrive(bar(kVFull, b));
       }
       if (j + 1 < count) {
-        fetch(a.c.v, next, blk_next, raw_v);
+        fetch(a.c.v, blk_next, raw_v);
         blk[0] = blk_next[0];
         blk[1] = blk_next[1];
         if (j + 2 < count) {
-          ALHR_STEP(next);
-          blocks_of(next, blk_next);
+          step();
+          blocks_of(blk_next);
         }
       }
     }
@@ -714,77 +735,76 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   } else {
     fewer_registers<kProductRegs>();
   }
-  if (warp == 12) {
-    // ================ products: the warp waits together, one lane asks for them
+  if (warp == 12 || warp == 13) {
+    // ================ products: one warp for each tile of rows; it waits together, one lane asks
+    const int i = warp - 12;
     constexpr uint32_t kRowGroup = kCols * 128;  // bytes between groups of eight rows
     constexpr uint32_t kScore = product_desc(128, false), kSum = product_desc(D, true);
-    uint32_t phases = 0;  // bit i: of Q of tile i of rows, bit 2 + i: of its weights
-    int subs = cur.rows_here() > 128 ? 2 : 1;
-    // scores of tile j for tile i of rows
-    auto ask = [&](int i, int j, bool fresh) {
-      if (fresh) {
-        if (!warp_wait(bar(kQFull, i), (phases >> i) & 1u, stop)) return false;
-        phases ^= 1u << i;
-      }
-      if (!warp_wait(bar(kKFull, j & 1), (j >> 1) & 1, stop)) return false;
-      fence_after();
-      const uint64_t q = operand_desc(smem + L::q + i * L::kTile, 128, kRowGroup);
-      const uint64_t k = operand_desc(smem + L::k + (j & 1) * L::kTile, 128, kRowGroup);
-      if (elected()) {
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s)
-          product_ss(tmem + i * 128, q + s * 16, k + s * 16, kScore, s > 0);
-        commit_to(bar(kSFull, i));
-      }
-      __syncwarp();
-      return true;
-    };
-    // Step j sums tile j and asks for the scores of tile j + 1 (step -1: of tile 0 alone), so that
-    // one tile of rows takes its weights while the products of the other one run.
-    bool ok = true, add = false;
+    const uint64_t q_op = operand_desc(smem + L::q + i * L::kTile, 128, kRowGroup);
+    const uint64_t k_op = operand_desc(smem + L::k, 128, kRowGroup);
+    const uint64_t v_op = operand_desc(smem + L::v, kRowGroup, 128);
+    const uint32_t s_at = tmem + i * 128, o_at = tmem + 256 + i * D;
+    int left = cur.tiles - cur.tile + 1, units = 0, j_on = 0;
+    bool on = cur.rows_here() > i * 128, on_next = on, ok = true, add = false;
+    // Step j sums tile j and asks for the scores of tile j + 1 (step -1: of tile 0 alone). What the
+    // rows are not needed for is waited for first: keys and values are there long before.
 #pragma unroll 1
-    for (int j = -1; j < count && ok; ++j) {
-      const bool last = j < 0 || cur.tile + 1 == cur.tiles;
-      ChunkCursor after = cur;
-      if (j >= 0 && j + 1 < count) ALHR_STEP(after);
-      const int subs_after = after.rows_here() > 128 ? 2 : 1;
-#pragma unroll 1
-      for (int i = 0; i < 2 && ok; ++i) {
-        if (j >= 0 && i < subs) {
-          ok = warp_wait(bar(kPFull, i), (phases >> (2 + i)) & 1u, stop);
-          phases ^= 4u << i;
-          if (ok && i == 0) ok = warp_wait(bar(kVFull, j & 1), (j >> 1) & 1, stop);
-          if (!ok) break;
+    for (int j = -1; j < count; ++j) {
+      const bool more = j + 1 < count;
+      const bool last = --left == 0 || j < 0;  // tile j is its unit's last one
+      if (j >= 0 && last && more) {
+        const ChunkCursor c = next_unit(a, cursor, row_limit);
+        left = c.tiles;
+        on_next = c.rows_here() > i * 128;
+      }
+      if (more && !(ok = warp_wait(bar(kKFull, (j + 1) & 1), ((j + 1) >> 1) & 1, stop))) break;
+      if (j >= 0) {
+        if (!(ok = warp_wait(bar(kVFull, j & 1), (j >> 1) & 1, stop))) break;
+        if (on) {
+          if (!(ok = warp_wait(bar(kPFull, i), j_on & 1, stop))) break;
+          ++j_on;
           fence_after();
-          const uint64_t v = operand_desc(smem + L::v + (j & 1) * L::kTile, kRowGroup, 128);
+          const uint64_t v = v_op + (j & 1) * (L::kTile / 16);
           if (elected()) {
 #pragma unroll
             for (int s = 0; s < kKeys / 16; ++s)
-              product_ts(tmem + 256 + i * D, tmem + i * 128 + s * 8, v + s * (2 * kRowGroup / 16),
-                         kSum, add || s > 0);
-            if (last || j + 1 == count) commit_to(bar(kODone, i));
-            if (i == subs - 1) commit_to(bar(kVEmpty, j & 1));
+              product_ts(o_at, s_at + s * 8, v + s * (2 * kRowGroup / 16), kSum, add || s > 0);
+            commit_to(bar(kVEmpty, j & 1));
+            if (last || !more) commit_to(bar(kODone, i));
           }
           __syncwarp();
+        } else if (lane == 0) {
+          bar_arrive(bar(kVEmpty, j & 1));
         }
-        if (j + 1 < count && i < subs_after) {
-          ok = ask(i, j + 1, last);
-          if (ok && i == subs_after - 1) {
-            if (elected()) commit_to(bar(kKEmpty, (j + 1) & 1));
-            __syncwarp();
+      }
+      if (more) {
+        if (on_next) {
+          if (last) {
+            if (!(ok = warp_wait(bar(kQFull, i), units & 1, stop))) break;
+            ++units;
           }
+          fence_after();
+          const uint64_t k = k_op + ((j + 1) & 1) * (L::kTile / 16);
+          if (elected()) {
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+              product_ss(s_at, q_op + s * 16, k + s * 16, kScore, s > 0);
+            commit_to(bar(kSFull, i));
+            commit_to(bar(kKEmpty, (j + 1) & 1));
+          }
+          __syncwarp();
+        } else if (lane == 0) {
+          bar_arrive(bar(kKEmpty, (j + 1) & 1));
         }
       }
       add = !last;
-      cur = after;
-      subs = subs_after;
+      on = on_next;
     }
     if (!ok) {  // products in flight end before the tensor memory is freed
-      if (elected()) commit_to(bar(kDrain));
+      if (elected()) commit_to(bar(kDrain, i));
       __syncwarp();
-      *stop = 0;
-      warp_wait(bar(kDrain), 0, stop);
-      *stop = 1;
+      volatile int none = 0;
+      warp_wait(bar(kDrain, i), 0, &none);
     }
   }
   __syncwarp();
