@@ -9,7 +9,7 @@
 // 128. Four warps load codes to registers, widen them to halves (exact) and write them to shared
 // memory in the core-matrix layout of tcgen05 (8 rows of 16 bytes): for the keys (rows of the
 // second operand) K-major, and the same bytes read MN-major are the values' operand, so nothing is
-// transposed. Two warps ask for the products: S_i = Q_i K^T into tensor memory, and O_i += P_i V
+// transposed. One warp asks for the products: S_i = Q_i K^T into tensor memory, and O_i += P_i V
 // with P_i read from tensor memory, where the rows' threads put it in place of S_i. While the
 // tensor core works on one tile of rows the threads of the other one take their powers of two.
 // Rows of a request are (token, head of the group) pairs, so that grouped heads share every key
@@ -31,12 +31,13 @@ namespace {
 
 constexpr int kRows = 256;       // query rows of a unit: two tiles of 128
 constexpr int kKeys = 128;       // keys of a tile
-constexpr int kChunkThreads = 512;  // warps 0-3, 4-7: rows; 8-11: keys and values; 12, 13: products
+// Warps 0-3, 4-7: rows; 8-11: keys; 12-15: values; 16: products (17-19: none).
+constexpr int kChunkThreads = 640, kProductWarp = 16;
 constexpr uint32_t kWaits = 1u << 24;
 constexpr float kTopLog = 7.f;   // log2 of the largest weight when M is set
-// Registers of a thread of the rows', the codes' and the products' warps: 2 * 152 + 120 + 88 =
-// 4 * 128, what the block is launched with.
-constexpr int kRowRegs = 152, kCodeRegs = 120, kProductRegs = 88;
+// Registers of a thread of the rows', the codes' and the products' warps: 2 * 152 + 2 * 64 + 48 =
+// 5 * 96, what the block is launched with.
+constexpr int kRowRegs = 152, kCodeRegs = 64, kProductRegs = 48;
 
 template <int D>
 struct ChunkSmem {
@@ -62,6 +63,7 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 // Waits for the completion of the phase of this parity; false when the wait runs out or another
 // role has given up.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
+#pragma unroll 1
   for (uint32_t i = 0; i < kWaits; ++i) {
     uint32_t done;
     asm volatile(
@@ -208,6 +210,7 @@ struct ChunkRequest {
   }
   __device__ __forceinline__ long long per_head(const AttendArgs& a) const {
     long long n = 0;
+#pragma unroll 1
     for (int g = 0; g < groups; ++g) n += tiles(a, g);
     return n;
   }
@@ -304,7 +307,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (lane == 0) cursors[warp] = cur;
   ChunkCursor* const cursor = &cursors[warp];
 
-  if (warp == 12) {
+  if (warp == kProductWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
                      shared_u32(tmem_slot)),
                  "r"(512)
@@ -314,16 +317,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       bar_init(bar(kKFull, i), 4);
-      bar_init(bar(kKEmpty, i), 2);
+      bar_init(bar(kKEmpty, i), 1);
       bar_init(bar(kVFull, i), 4);
-      bar_init(bar(kVEmpty, i), 2);
+      bar_init(bar(kVEmpty, i), 1);
       bar_init(bar(kScFree, i), 8);
       bar_init(bar(kSFull, i), 1);
       bar_init(bar(kPFull, i), 4);
       bar_init(bar(kQFull, i), 4);
       bar_init(bar(kODone, i), 1);
-      bar_init(bar(kDrain, i), 1);
     }
+    bar_init(bar(kDrain), 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     *stop = 0;
   }
@@ -605,129 +608,110 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       fresh = left == 0 || j + 1 == count;
       seen -= kKeys;
     }
-  } else if (warp < 12) {
-    // ================ keys and values: codes to halves
+  } else if (warp < kProductWarp) {
+    // ================ codes to halves: keys (and the scales) or values
     fewer_registers<kCodeRegs>();
-    const int w = warp - 8;
+    const int w = warp & 3;
+    const bool keys = warp < 12;
+    const uint8_t* const codes = keys ? a.c.k : a.c.v;
+    const uint32_t full = bar(keys ? kKFull : kVFull), empty = bar(keys ? kKEmpty : kVEmpty);
     const int kr = lane & 7, kc = lane >> 3;       // row of eight, 16-byte piece of 64
     constexpr int kHalves = D / 64;                // pieces kc, kc + 4
+    const uint32_t dst0 = smem + (keys ? L::k : L::v) + w * 4 * (kCols * 128) + kc * 256 + kr * 16;
     bool bad = false;
-    // the tile whose codes are asked for
+    // the tile whose codes are asked for, this warp's 32 keys of it
     int key0 = cur.tile * kKeys + w * 32, key_end = cur.q.see, left = cur.tiles - cur.tile;
     int head = cur.h;
     const int32_t* table = a.table + static_cast<long long>(cur.r) * a.max_blocks;
-    auto step = [&]() {
-      key0 += kKeys;
-      if (--left) return;
-      const ChunkCursor c = next_unit(a, cursor, row_limit);
-      key0 = w * 32;
-      key_end = c.q.see;
-      left = c.tiles;
-      head = c.h;
-      table = a.table + static_cast<long long>(c.r) * a.max_blocks;
+    int blk_next[2];  // table entries of its two 16-key groups, -1 where no key is visible
+    auto look_up = [&]() {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        blk_next[u] = key0 + u * 16 < key_end ? __ldg(table + ((key0 + u * 16) >> a.c.bs_log)) : -1;
     };
-    // blocks of the two 16-key groups of this warp's 32 keys
-    auto blocks_of = [&](int (&blk)[2]) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int key = key0 + u * 16;
-        blk[u] = -1;
-        if (key < key_end) {
-          blk[u] = __ldg(table + (key >> a.c.bs_log));
-          if (blk[u] < 0 || blk[u] >= a.c.blocks) {
-            blk[u] = -1;
-            bad = true;
-          }
-        }
-      }
-    };
-    auto fetch = [&](const uint8_t* codes, const int (&blk)[2], uint4 (&raw)[4 * kHalves]) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int key = key0 + u * 16;
-        const long long row = block_row(a.c, max(blk[u], 0), head) + (key & (a.c.bs - 1)) + kr;
-        const uint8_t* p = codes + row * D + kc * 16;
-        const int there = blk[u] < 0 ? 0 : key_end - key - kr;  // this lane's rows 0 and 8
-#pragma unroll
-        for (int rg = 0; rg < 2; ++rg)
-#pragma unroll
-          for (int hh = 0; hh < kHalves; ++hh)
-            raw[(u * 2 + rg) * kHalves + hh] =
-                there > rg * 8 ? __ldg(reinterpret_cast<const uint4*>(p + rg * 8 * D + hh * 64))
-                              : make_uint4(0u, 0u, 0u, 0u);
-      }
-    };
-    // lanes 0, 1: scales of this warp's two groups
-    float ks = 0.f, vs = 0.f;
-    auto fetch_scales = [&](const int (&blk)[2]) {
-      const int mine = lane == 0 ? blk[0] : blk[1];
-      ks = vs = 0.f;
-      if (lane < 2 && mine >= 0) {
-        const long long si = static_cast<long long>(mine) * a.c.heads + head;
-        ks = __ldg(a.c.k_scale + si);
-        vs = __ldg(a.c.v_scale + si);
-      }
-    };
-    auto widen = [&](uint32_t dst, const uint4 (&raw)[4 * kHalves]) {
-#pragma unroll
-      for (int rg = 0; rg < 4; ++rg)
-#pragma unroll
-        for (int hh = 0; hh < kHalves; ++hh) {
-          const uint4 x = raw[rg * kHalves + hh];
-          uint32_t y[8];
-          widen4<CODE>(x.x, y[0], y[1]);
-          widen4<CODE>(x.y, y[2], y[3]);
-          widen4<CODE>(x.z, y[4], y[5]);
-          widen4<CODE>(x.w, y[6], y[7]);
-          const uint32_t at = dst + ((w * 4 + rg) * kCols + (kc + hh * 4) * 2) * 128 + kr * 16;
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(at), "r"(y[0]), "r"(y[1]),
-                       "r"(y[2]), "r"(y[3])
-                       : "memory");
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(at + 128), "r"(y[4]),
-                       "r"(y[5]), "r"(y[6]), "r"(y[7])
-                       : "memory");
-        }
-    };
-    uint4 raw_k[4 * kHalves], raw_v[4 * kHalves];
-    int blk[2] = {-1, -1}, blk_next[2];
-    blocks_of(blk_next);
+    uint4 raw[4 * kHalves];
+    float ks = 0.f, vs = 0.f;  // lanes 0, 1: scales of the two groups, and whether they count
+    bool there = false;
+    look_up();
 #pragma unroll 1
     for (int j = -1; j < count; ++j) {  // tile j is widened, tile j + 1 asked for
       const int b = j & 1;
       if (j >= 0) {
         if (j >= 2) {
-          if (!warp_wait(bar(kKEmpty, b), ((j >> 1) - 1) & 1, stop)) break;
-          if (!warp_wait(bar(kScFree, b), ((j >> 1) - 1) & 1, stop)) break;
+          if (!warp_wait(empty + b * 8, ((j >> 1) - 1) & 1, stop)) break;
+          if (keys && !warp_wait(bar(kScFree, b), ((j >> 1) - 1) & 1, stop)) break;
         }
-        widen(smem + L::k + b * L::kTile, raw_k);
-        if (lane < 2) {
+        const uint32_t dst = dst0 + b * L::kTile;
+#pragma unroll
+        for (int rg = 0; rg < 4; ++rg)
+#pragma unroll
+          for (int hh = 0; hh < kHalves; ++hh) {
+            const uint4 x = raw[rg * kHalves + hh];
+            uint32_t y[8];
+            widen4<CODE>(x.x, y[0], y[1]);
+            widen4<CODE>(x.y, y[2], y[3]);
+            widen4<CODE>(x.z, y[4], y[5]);
+            widen4<CODE>(x.w, y[6], y[7]);
+            const uint32_t at = dst + (rg * kCols + hh * 8) * 128;
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(at), "r"(y[0]), "r"(y[1]),
+                         "r"(y[2]), "r"(y[3])
+                         : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(at + 128), "r"(y[4]),
+                         "r"(y[5]), "r"(y[6]), "r"(y[7])
+                         : "memory");
+          }
+        if (keys && lane < 2) {
           const float v1 = fmaxf(vs, kTinyScale);
           float4 f = make_float4(ks, __log2f(v1), __frcp_rn(v1), 0.f);
-          if ((lane == 0 ? blk[0] : blk[1]) < 0) f = make_float4(0.f, -INFINITY, 0.f, 0.f);
+          if (!there) f = make_float4(0.f, -INFINITY, 0.f, 0.f);
           reinterpret_cast<float4*>(chunk_smem + L::scales)[b * 8 + w * 2 + lane] = f;
         }
         fence_shared();
         __syncwarp();
-        if (lane == 0) bar_arrive(bar(kKFull, b));
+        if (lane == 0) bar_arrive(full + b * 8);
       }
       if (j + 1 < count) {
-        fetch_scales(blk_next);
-        fetch(a.c.k, blk_next, raw_k);
-      }
-      if (j >= 0) {
-        if (j >= 2 && !warp_wait(bar(kVEmpty, b), ((j >> 1) - 1) & 1, stop)) break;
-        widen(smem + L::v + b * L::kTile, raw_v);
-        fence_shared();
-        __syncwarp();
-        if (lane == 0) bar_arrive(bar(kVFull, b));
-      }
-      if (j + 1 < count) {
-        fetch(a.c.v, blk_next, raw_v);
-        blk[0] = blk_next[0];
-        blk[1] = blk_next[1];
+        int blk[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          blk[u] = blk_next[u];
+          if (blk[u] < 0 || blk[u] >= a.c.blocks) {
+            if (key0 + u * 16 < key_end) bad = true;
+            blk[u] = -1;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int key = key0 + u * 16;
+          const long long row = block_row(a.c, max(blk[u], 0), head) + (key & (a.c.bs - 1)) + kr;
+          const uint8_t* p = codes + row * D + kc * 16;
+          const int rows = blk[u] < 0 ? 0 : key_end - key - kr;  // this lane's rows 0 and 8
+#pragma unroll
+          for (int rg = 0; rg < 2; ++rg)
+#pragma unroll
+            for (int hh = 0; hh < kHalves; ++hh)
+              raw[(u * 2 + rg) * kHalves + hh] =
+                  rows > rg * 8 ? __ldg(reinterpret_cast<const uint4*>(p + rg * 8 * D + hh * 64))
+                                : make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (keys && lane < 2) {
+          const int mine = lane == 0 ? blk[0] : blk[1];
+          const long long si = static_cast<long long>(max(mine, 0)) * a.c.heads + head;
+          there = mine >= 0;
+          ks = there ? __ldg(a.c.k_scale + si) : 0.f;
+          vs = there ? __ldg(a.c.v_scale + si) : 0.f;
+        }
         if (j + 2 < count) {
-          step();
-          blocks_of(blk_next);
+          key0 += kKeys;
+          if (--left == 0) {
+            const ChunkCursor c = next_unit(a, cursor, row_limit);
+            key0 = w * 32;
+            key_end = c.q.see;
+            left = c.tiles;
+            head = c.h;
+            table = a.table + static_cast<long long>(c.r) * a.max_blocks;
+          }
+          look_up();
         }
       }
     }
@@ -735,19 +719,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   } else {
     fewer_registers<kProductRegs>();
   }
-  if (warp == 12 || warp == 13) {
-    // ================ products: one warp for each tile of rows; it waits together, one lane asks
-    const int i = warp - 12;
+  if (warp == kProductWarp) {
+    // ================ products: the warp waits together, one lane asks for them
     constexpr uint32_t kRowGroup = kCols * 128;  // bytes between groups of eight rows
     constexpr uint32_t kScore = product_desc(128, false), kSum = product_desc(D, true);
-    const uint64_t q_op = operand_desc(smem + L::q + i * L::kTile, 128, kRowGroup);
+    const uint64_t q_op = operand_desc(smem + L::q, 128, kRowGroup);
     const uint64_t k_op = operand_desc(smem + L::k, 128, kRowGroup);
     const uint64_t v_op = operand_desc(smem + L::v, kRowGroup, 128);
-    const uint32_t s_at = tmem + i * 128, o_at = tmem + 256 + i * D;
-    int left = cur.tiles - cur.tile + 1, units = 0, j_on = 0;
-    bool on = cur.rows_here() > i * 128, on_next = on, ok = true, add = false;
-    // Step j sums tile j and asks for the scores of tile j + 1 (step -1: of tile 0 alone). What the
-    // rows are not needed for is waited for first: keys and values are there long before.
+    int left = cur.tiles - cur.tile + 1;
+    uint32_t phases = 0;  // bit i: of Q of tile i of rows, bit 2 + i: of its weights
+    int subs = cur.rows_here() > 128 ? 2 : 1, subs_next = subs;
+    bool ok = true, add = false;
+    // Step j sums tile j and asks for the scores of tile j + 1 (step -1: of tile 0 alone), first of
+    // one tile of rows, then of the other: while the second one's products run, the first one's
+    // rows take their weights, and the two stay out of step. What the rows are not needed for is
+    // waited for first: keys and values are there long before.
 #pragma unroll 1
     for (int j = -1; j < count; ++j) {
       const bool more = j + 1 < count;
@@ -755,63 +741,61 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (j >= 0 && last && more) {
         const ChunkCursor c = next_unit(a, cursor, row_limit);
         left = c.tiles;
-        on_next = c.rows_here() > i * 128;
+        subs_next = c.rows_here() > 128 ? 2 : 1;
       }
       if (more && !(ok = warp_wait(bar(kKFull, (j + 1) & 1), ((j + 1) >> 1) & 1, stop))) break;
-      if (j >= 0) {
-        if (!(ok = warp_wait(bar(kVFull, j & 1), (j >> 1) & 1, stop))) break;
-        if (on) {
-          if (!(ok = warp_wait(bar(kPFull, i), j_on & 1, stop))) break;
-          ++j_on;
+      if (j >= 0 && !(ok = warp_wait(bar(kVFull, j & 1), (j >> 1) & 1, stop))) break;
+      const uint64_t k = k_op + ((j + 1) & 1) * (L::kTile / 16);
+      const uint64_t v = v_op + (j & 1) * (L::kTile / 16);
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t s_at = tmem + i * 128, o_at = tmem + 256 + i * D;
+        if (j >= 0 && i < subs) {
+          if (!(ok = warp_wait(bar(kPFull, i), (phases >> (2 + i)) & 1u, stop))) break;
+          phases ^= 4u << i;
           fence_after();
-          const uint64_t v = v_op + (j & 1) * (L::kTile / 16);
           if (elected()) {
 #pragma unroll
             for (int s = 0; s < kKeys / 16; ++s)
               product_ts(o_at, s_at + s * 8, v + s * (2 * kRowGroup / 16), kSum, add || s > 0);
-            commit_to(bar(kVEmpty, j & 1));
             if (last || !more) commit_to(bar(kODone, i));
+            if (i == subs - 1) commit_to(bar(kVEmpty, j & 1));
           }
           __syncwarp();
-        } else if (lane == 0) {
-          bar_arrive(bar(kVEmpty, j & 1));
         }
-      }
-      if (more) {
-        if (on_next) {
+        if (more && i < subs_next) {
           if (last) {
-            if (!(ok = warp_wait(bar(kQFull, i), units & 1, stop))) break;
-            ++units;
+            if (!(ok = warp_wait(bar(kQFull, i), (phases >> i) & 1u, stop))) break;
+            phases ^= 1u << i;
+            fence_after();
           }
-          fence_after();
-          const uint64_t k = k_op + ((j + 1) & 1) * (L::kTile / 16);
           if (elected()) {
+            const uint64_t q = q_op + i * (L::kTile / 16);
 #pragma unroll
             for (int s = 0; s < D / 16; ++s)
-              product_ss(s_at, q_op + s * 16, k + s * 16, kScore, s > 0);
+              product_ss(s_at, q + s * 16, k + s * 16, kScore, s > 0);
             commit_to(bar(kSFull, i));
-            commit_to(bar(kKEmpty, (j + 1) & 1));
+            if (i == subs_next - 1) commit_to(bar(kKEmpty, (j + 1) & 1));
           }
           __syncwarp();
-        } else if (lane == 0) {
-          bar_arrive(bar(kKEmpty, (j + 1) & 1));
         }
       }
+      if (!ok) break;
       add = !last;
-      on = on_next;
+      subs = subs_next;
     }
     if (!ok) {  // products in flight end before the tensor memory is freed
-      if (elected()) commit_to(bar(kDrain, i));
+      if (elected()) commit_to(bar(kDrain));
       __syncwarp();
       volatile int none = 0;
-      warp_wait(bar(kDrain, i), 0, &none);
+      warp_wait(bar(kDrain), 0, &none);
     }
   }
   __syncwarp();
   fence_before();
   __syncthreads();
   if (tid == 0 && *stop) cache_flag(a.dev_err, ALHR_DEVERR_TIMEOUT);
-  if (warp == 12)
+  if (warp == kProductWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512)
                  : "memory");
 }
