@@ -9,7 +9,8 @@
 // 128. Four warps load codes to registers, widen them to halves (exact) and write them to shared
 // memory in the core-matrix layout of tcgen05 (8 rows of 16 bytes): for the keys (rows of the
 // second operand) K-major, and the same bytes read MN-major are the values' operand, so nothing is
-// transposed. One warp asks for the products: S_i = Q_i K^T into tensor memory, and O_i += P_i V
+// transposed. One lane of each tile of rows asks
+// for its products: S_i = Q_i K^T into tensor memory, and O_i += P_i V
 // with P_i read from tensor memory, where the rows' threads put it in place of S_i. While the
 // tensor core works on one tile of rows the threads of the other one take their powers of two.
 // Rows of a request are (token, head of the group) pairs, so that grouped heads share every key
@@ -18,8 +19,9 @@
 // As in cache_decode.cu the key tiles of all units form one list of which every CTA takes an
 // equal, contiguous piece; units that span pieces leave partial sums that a second kernel joins.
 //
-// Every wait is bounded; when one runs out (not expected) the CTA stops, sets ALHR_DEVERR_TIMEOUT,
-// waits (bounded) for its products in flight and frees its tensor memory.
+// Every wait is bounded; when one runs out (not expected) the CTA sets ALHR_DEVERR_TIMEOUT and stops
+// waiting (its rows' output is then not to be used), lets its products in flight end (bounded) and
+// frees its tensor memory.
 #include <cmath>
 
 #include "cache_mma.cuh"
@@ -31,13 +33,13 @@ namespace {
 
 constexpr int kRows = 256;       // query rows of a unit: two tiles of 128
 constexpr int kKeys = 128;       // keys of a tile
-// Warps 0-3, 4-7: rows; 8-11: keys; 12-15: values; 16: products (17-19: none).
-constexpr int kChunkThreads = 640, kProductWarp = 16;
+// Warps 0-3, 4-7: the two tiles of rows; 8-11: keys; 12-15: values.
+constexpr int kChunkThreads = 512;
 constexpr uint32_t kWaits = 1u << 24;
 constexpr float kTopLog = 7.f;   // log2 of the largest weight when M is set
-// Registers of a thread of the rows', the codes' and the products' warps: 2 * 152 + 2 * 64 + 48 =
-// 5 * 96, what the block is launched with.
-constexpr int kRowRegs = 152, kCodeRegs = 64, kProductRegs = 48;
+// Registers of a thread of the rows' and the codes' warps: 2 * 160 + 2 * 96 = 4 * 128, what the
+// block is launched with.
+constexpr int kRowRegs = 160, kCodeRegs = 96;
 
 template <int D>
 struct ChunkSmem {
@@ -45,13 +47,13 @@ struct ChunkSmem {
   static constexpr int q = 0;                    // two tiles
   static constexpr int k = 2 * kTile;            // two tiles
   static constexpr int v = 4 * kTile;            // two tiles
-  static constexpr int scales = 6 * kTile;       // [2][8] of {k scale, log2 v scale, 1 / v scale}
-  static constexpr int bars = scales + 2 * 8 * 16;
+  static constexpr int scales = 6 * kTile;       // [4][8] of {k scale, log2 v scale, 1 / v scale}
+  static constexpr int bars = scales + 4 * 8 * 16;
   static constexpr int misc = bars + 32 * 8;
   static constexpr int bytes = misc + 64;
 };
 
-enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kScFree = 8, kSFull = 10, kPFull = 12,
+enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kTurn = 8, kSFull = 10, kPFull = 12,
            kQFull = 14, kODone = 16, kDrain = 18 };
 
 __device__ __forceinline__ void bar_init(uint32_t bar, int count) {
@@ -60,28 +62,31 @@ __device__ __forceinline__ void bar_init(uint32_t bar, int count) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
-// Waits for the completion of the phase of this parity; false when the wait runs out or another
-// role has given up.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
+// The warp waits for the completion of the phase of this parity. When the wait runs out, *stop is
+// set and every later wait of the block returns at once: its roles then run to the end of their
+// loops with whatever the buffers hold (all inside them), together as always.
+__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  if (!done) {
 #pragma unroll 1
-  for (uint32_t i = 0; i < kWaits; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (done) return true;
-    if ((i & 63u) == 63u && *stop) return false;
+    for (uint32_t i = 0; i < kWaits; ++i) {
+      asm volatile(
+          "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+          " selp.u32 %0, 1, 0, p;\n}\n"
+          : "=r"(done)
+          : "r"(bar), "r"(parity)
+          : "memory");
+      if (done || ((i & 15u) == 15u && *stop)) break;
+    }
+    if (!done) *stop = 1;
   }
-  *stop = 1;
-  return false;
-}
-
-// The same for a whole warp: all of its lanes go on, or none.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
-  return __all_sync(0xffffffffu, bar_wait(bar, parity, stop));
+  __syncwarp();
 }
 
 // Shared-memory operand descriptor without swizzle: start address, leading and stride byte offset.
@@ -255,6 +260,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                  const int row_limit) {
   using L = ChunkSmem<D>;
   constexpr int kCols = D / 8;  // 16-byte columns of a row of halves
+  // At d = 128 the two tiles of rows take turns with the tensor core and so stay out of step (1.11
+  // ms against 1.13 for 2 x 2048 rows x 32 heads behind 14,336 keys); at d = 64 its products are
+  // short and waiting for a turn costs more (258 us against 277 for prompts of 301 to 4096 tokens).
+  constexpr bool kTurns = D == 128;
   extern __shared__ __align__(1024) unsigned char chunk_smem[];
   __shared__ long long chunk_start[kChunkThreads];
   __shared__ long long warp_sum[kChunkThreads / 32];
@@ -307,7 +316,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (lane == 0) cursors[warp] = cur;
   ChunkCursor* const cursor = &cursors[warp];
 
-  if (warp == kProductWarp) {
+  if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
                      shared_u32(tmem_slot)),
                  "r"(512)
@@ -317,18 +326,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       bar_init(bar(kKFull, i), 4);
-      bar_init(bar(kKEmpty, i), 1);
+      bar_init(bar(kKEmpty, i), 2);
       bar_init(bar(kVFull, i), 4);
-      bar_init(bar(kVEmpty, i), 1);
-      bar_init(bar(kScFree, i), 8);
-      bar_init(bar(kSFull, i), 1);
+      bar_init(bar(kVEmpty, i), 2);
+      bar_init(bar(kTurn, i), 1);
+      bar_init(bar(kSFull, i), 2);
       bar_init(bar(kPFull, i), 4);
       bar_init(bar(kQFull, i), 4);
       bar_init(bar(kODone, i), 1);
+      bar_init(bar(kDrain, i), 1);
     }
-    bar_init(bar(kDrain), 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     *stop = 0;
+    bar_arrive(bar(kTurn, 0));  // the first tile of rows begins
   }
   fence_before();
   __syncthreads();
@@ -396,9 +406,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       __syncwarp();
       if (lane == 0) bar_arrive(bar(kQFull, i));
     };
+    // ---- products, asked for by one lane of the tile's first warp
+    const bool asks = (warp & 3) == 0;
+    constexpr uint32_t kRowGroup = kCols * 128;  // bytes between groups of eight rows
+    constexpr uint32_t kScore = product_desc(128, false), kSum = product_desc(D, true);
+    const uint32_t s_at = tmem + i * 128, o_at = tmem + 256 + i * D;
+    auto ask_scores = [&](int j) {  // of key tile j; the warp's elected lane
+      const uint64_t q = operand_desc(smem + L::q + i * L::kTile, 128, kRowGroup);
+      const uint64_t k = operand_desc(smem + L::k + (j & 1) * L::kTile, 128, kRowGroup);
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) product_ss(s_at, q + s * 16, k + s * 16, kScore, s > 0);
+      commit_to(bar(kSFull, i));
+      commit_to(bar(kKEmpty, j & 1));
+      bar_arrive(bar(kSFull, i));  // hands on that the tile's scales are there
+    };
     bool first = true, fresh = true, from_start = true, busy = false;
-    int units = 0, left = 0;  // key tiles of the unit that are still to come
-    uint32_t s_phase = 0;
+    int units = 0, q_units = 0, left = 0;  // key tiles of the unit that are still to come
+    uint32_t s_phase = 0, p_phase = 0;
     for (int j = 0;; ++j) {
       if (fresh) {
         // ---- the unit before (or this piece of it) has ended, another one begins
@@ -424,9 +448,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           // S of the last tile is here, so nothing reads the queries before any more
           if (busy) load_q(now);
           seen -= now.tile * kKeys;
+          if (asks) {
+            warp_wait(bar(kKFull, j & 1), (j >> 1) & 1, stop);
+            if (busy) {
+              warp_wait(bar(kQFull, i), q_units & 1, stop);
+              ++q_units;
+              fence_after();
+              if (elected()) ask_scores(j);
+              __syncwarp();
+            } else if (lane == 0) {
+              bar_arrive(bar(kKEmpty, j & 1));
+            }
+          }
         }
         if (j > 0 && was_busy) {
-          if (!warp_wait(bar(kODone, i), units & 1, stop)) break;
+          warp_wait(bar(kODone, i), units & 1, stop);
           ++units;
           fence_after();
           const bool on = was_row < was.q.rows, whole = started && to_end;
@@ -473,63 +509,58 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
       }
       if (j == count) break;
-      const int b = j & 1;
-      if (!warp_wait(bar(kKFull, b), (j >> 1) & 1, stop)) break;
-      if (!busy) {
-        __syncwarp();
-        if (lane == 0) bar_arrive(bar(kScFree, b));
-      } else {
-        if (!warp_wait(bar(kSFull, i), s_phase, stop)) break;
+      if (busy) {
+        warp_wait(bar(kSFull, i), s_phase, stop);
         s_phase ^= 1u;
         fence_after();
         const bool cut = __any_sync(0xffffffffu, seen < kKeys);
-        const float4* sc = reinterpret_cast<const float4*>(scales) + b * 8;
+        const float4* sc = reinterpret_cast<const float4*>(scales) + (j & 3) * 8;
         // Nearly always M stays as it is: weights are taken with it at once, and held until it is
         // known that none is above 2^15. The tile in which M has to grow, the first one of a unit
         // and those that a mask cuts take two passes over the scores.
         bool done = false;
         if (!first && !cut) {
-          uint32_t kept[32], p[32];  // weights of columns 0-63, 64-127
+          uint32_t p[64];
           float sum = l, most = m == -INFINITY ? INFINITY : 0.f;
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
+          uint32_t v[2][32];
+          tmem_ld32(v[0], s_col);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) kept[k] = p[k];
-            uint32_t v[2][32];
-            tmem_ld32(v[0], s_col + h * 64);
+          for (int c = 0; c < 4; ++c) {
+            wait_ld();
+            if (c < 3) tmem_ld32(v[(c + 1) & 1], s_col + (c + 1) * 32);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              wait_ld();
-              if (c == 0) tmem_ld32(v[1], s_col + h * 64 + 32);
+            for (int u = 0; u < 2; ++u) {
+              const float4 f = sc[c * 2 + u];
+              const float f1 = qs * f.x, f0 = f.y - m;
+              const uint64_t f11 = pair(f1, f1), f00 = pair(f0, f0);
+              uint64_t part = 0;
 #pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const float4 f = sc[h * 4 + c * 2 + u];
-                const float f1 = qs * f.x, f0 = f.y - m;
-                const uint64_t f11 = pair(f1, f1), f00 = pair(f0, f0);
-                uint64_t part = 0;
-#pragma unroll
-                for (int k = 0; k < 16; k += 2) {
-                  const uint32_t* w = &v[c][u * 16 + k];
-                  float x0, x1;
-                  unpair(fma2(pair(__uint_as_float(w[0]), __uint_as_float(w[1])), f11, f00), x0, x1);
-                  x0 = exp2_fast(x0);
-                  x1 = exp2_fast(x1);
-                  part = add2(part, pair(x0, x1));
-                  p[c * 16 + u * 8 + k / 2] = pack2(x0, x1, true);
-                }
-                float lo, hi;
-                unpair(part, lo, hi);
-                lo += hi;
-                most = fmaxf(most, lo);
-                sum = fmaf(lo, f.z, sum);
+              for (int k = 0; k < 16; k += 2) {
+                const uint32_t* w = &v[c & 1][u * 16 + k];
+                float x0, x1;
+                unpair(fma2(pair(__uint_as_float(w[0]), __uint_as_float(w[1])), f11, f00), x0, x1);
+                x0 = exp2_fast(x0);
+                x1 = exp2_fast(x1);
+                part = add2(part, pair(x0, x1));
+                p[c * 16 + u * 8 + k / 2] = pack2(x0, x1, true);
               }
+              float lo, hi;
+              unpair(part, lo, hi);
+              lo += hi;
+              most = fmaxf(most, lo);
+              sum = fmaf(lo, f.z, sum);
             }
           }
           done = __all_sync(0xffffffffu, most <= 32768.f);
           if (done) {
             l = sum;
-            tmem_st32(s_col, kept);
-            tmem_st32(s_col + 32, p);
+            uint32_t half[32];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) half[k] = p[h * 32 + k];
+              tmem_st32(s_col + h * 32, half);
+            }
           }
         }
         if (!done) {
@@ -598,17 +629,49 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         wait_st();
         fence_before();
         __syncwarp();
-        if (lane == 0) {
-          bar_arrive(bar(kScFree, b));
-          bar_arrive(bar(kPFull, i));
-        }
+        if (lane == 0) bar_arrive(bar(kPFull, i));
       }
-      first = false;
       --left;
       fresh = left == 0 || j + 1 == count;
       seen -= kKeys;
+      if (asks) {
+        // The sum of this tile and the scores of the next one, in turn with the other tile of rows:
+        // its rows take their weights while these products run. Keys and values are there before
+        // the weights are.
+        if (!fresh) warp_wait(bar(kKFull, (j + 1) & 1), ((j + 1) >> 1) & 1, stop);
+        warp_wait(bar(kVFull, j & 1), (j >> 1) & 1, stop);
+        if (busy) warp_wait(bar(kPFull, i), p_phase, stop);
+        if (kTurns) warp_wait(bar(kTurn, i), j & 1, stop);
+        if (busy) {
+          p_phase ^= 1u;
+          fence_after();
+          if (elected()) {
+            const uint64_t v = operand_desc(smem + L::v + (j & 1) * L::kTile, kRowGroup, 128);
+#pragma unroll
+            for (int s = 0; s < kKeys / 16; ++s)
+              product_ts(o_at, s_at + s * 8, v + s * (2 * kRowGroup / 16), kSum, !first || s > 0);
+            commit_to(bar(kVEmpty, j & 1));
+            if (fresh) commit_to(bar(kODone, i));
+            else ask_scores(j + 1);
+            bar_arrive(bar(kTurn, 1 - i));
+          }
+          __syncwarp();
+        } else if (lane == 0) {
+          bar_arrive(bar(kVEmpty, j & 1));
+          if (!fresh) bar_arrive(bar(kKEmpty, (j + 1) & 1));
+          bar_arrive(bar(kTurn, 1 - i));
+        }
+      }
+      first = false;
     }
-  } else if (warp < kProductWarp) {
+    __syncwarp();
+    if (asks && *stop) {  // products in flight end before the tensor memory is freed
+      if (elected()) commit_to(bar(kDrain, i));
+      __syncwarp();
+      volatile int none = 0;
+      warp_wait(bar(kDrain, i), 0, &none);
+    }
+  } else {
     // ================ codes to halves: keys (and the scales) or values
     fewer_registers<kCodeRegs>();
     const int w = warp & 3;
@@ -638,8 +701,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int b = j & 1;
       if (j >= 0) {
         if (j >= 2) {
-          if (!warp_wait(empty + b * 8, ((j >> 1) - 1) & 1, stop)) break;
-          if (keys && !warp_wait(bar(kScFree, b), ((j >> 1) - 1) & 1, stop)) break;
+          warp_wait(empty + b * 8, ((j >> 1) - 1) & 1, stop);
         }
         const uint32_t dst = dst0 + b * L::kTile;
 #pragma unroll
@@ -664,7 +726,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const float v1 = fmaxf(vs, kTinyScale);
           float4 f = make_float4(ks, __log2f(v1), __frcp_rn(v1), 0.f);
           if (!there) f = make_float4(0.f, -INFINITY, 0.f, 0.f);
-          reinterpret_cast<float4*>(chunk_smem + L::scales)[b * 8 + w * 2 + lane] = f;
+          // four tiles of scales: the rows are done with those of tile j - 3 before the scores of
+          // tile j - 2 are asked for, which the wait above has seen
+          reinterpret_cast<float4*>(chunk_smem + L::scales)[(j & 3) * 8 + w * 2 + lane] = f;
         }
         fence_shared();
         __syncwarp();
@@ -716,86 +780,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) cache_flag(a.dev_err, ALHR_DEVERR_BLOCK);
-  } else {
-    fewer_registers<kProductRegs>();
-  }
-  if (warp == kProductWarp) {
-    // ================ products: the warp waits together, one lane asks for them
-    constexpr uint32_t kRowGroup = kCols * 128;  // bytes between groups of eight rows
-    constexpr uint32_t kScore = product_desc(128, false), kSum = product_desc(D, true);
-    const uint64_t q_op = operand_desc(smem + L::q, 128, kRowGroup);
-    const uint64_t k_op = operand_desc(smem + L::k, 128, kRowGroup);
-    const uint64_t v_op = operand_desc(smem + L::v, kRowGroup, 128);
-    int left = cur.tiles - cur.tile + 1;
-    uint32_t phases = 0;  // bit i: of Q of tile i of rows, bit 2 + i: of its weights
-    int subs = cur.rows_here() > 128 ? 2 : 1, subs_next = subs;
-    bool ok = true, add = false;
-    // Step j sums tile j and asks for the scores of tile j + 1 (step -1: of tile 0 alone), first of
-    // one tile of rows, then of the other: while the second one's products run, the first one's
-    // rows take their weights, and the two stay out of step. What the rows are not needed for is
-    // waited for first: keys and values are there long before.
-#pragma unroll 1
-    for (int j = -1; j < count; ++j) {
-      const bool more = j + 1 < count;
-      const bool last = --left == 0 || j < 0;  // tile j is its unit's last one
-      if (j >= 0 && last && more) {
-        const ChunkCursor c = next_unit(a, cursor, row_limit);
-        left = c.tiles;
-        subs_next = c.rows_here() > 128 ? 2 : 1;
-      }
-      if (more && !(ok = warp_wait(bar(kKFull, (j + 1) & 1), ((j + 1) >> 1) & 1, stop))) break;
-      if (j >= 0 && !(ok = warp_wait(bar(kVFull, j & 1), (j >> 1) & 1, stop))) break;
-      const uint64_t k = k_op + ((j + 1) & 1) * (L::kTile / 16);
-      const uint64_t v = v_op + (j & 1) * (L::kTile / 16);
-#pragma unroll 1
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t s_at = tmem + i * 128, o_at = tmem + 256 + i * D;
-        if (j >= 0 && i < subs) {
-          if (!(ok = warp_wait(bar(kPFull, i), (phases >> (2 + i)) & 1u, stop))) break;
-          phases ^= 4u << i;
-          fence_after();
-          if (elected()) {
-#pragma unroll
-            for (int s = 0; s < kKeys / 16; ++s)
-              product_ts(o_at, s_at + s * 8, v + s * (2 * kRowGroup / 16), kSum, add || s > 0);
-            if (last || !more) commit_to(bar(kODone, i));
-            if (i == subs - 1) commit_to(bar(kVEmpty, j & 1));
-          }
-          __syncwarp();
-        }
-        if (more && i < subs_next) {
-          if (last) {
-            if (!(ok = warp_wait(bar(kQFull, i), (phases >> i) & 1u, stop))) break;
-            phases ^= 1u << i;
-            fence_after();
-          }
-          if (elected()) {
-            const uint64_t q = q_op + i * (L::kTile / 16);
-#pragma unroll
-            for (int s = 0; s < D / 16; ++s)
-              product_ss(s_at, q + s * 16, k + s * 16, kScore, s > 0);
-            commit_to(bar(kSFull, i));
-            if (i == subs_next - 1) commit_to(bar(kKEmpty, (j + 1) & 1));
-          }
-          __syncwarp();
-        }
-      }
-      if (!ok) break;
-      add = !last;
-      subs = subs_next;
-    }
-    if (!ok) {  // products in flight end before the tensor memory is freed
-      if (elected()) commit_to(bar(kDrain));
-      __syncwarp();
-      volatile int none = 0;
-      warp_wait(bar(kDrain), 0, &none);
-    }
   }
   __syncwarp();
   fence_before();
   __syncthreads();
   if (tid == 0 && *stop) cache_flag(a.dev_err, ALHR_DEVERR_TIMEOUT);
-  if (warp == kProductWarp)
+  if (warp == 8)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512)
                  : "memory");
 }
