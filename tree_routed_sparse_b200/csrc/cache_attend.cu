@@ -10,16 +10,20 @@ constexpr int kFewRows = 16;
 
 // max_rows: the most rows of one key head that a request may have.
 size_t attend_cache_workspace(int sms, int d, long long max_rows) {
-  const size_t few = decode_workspace(sms, d), many = chunk_workspace(sms, d);
-  return max_rows > kFewRows && many > few ? many : few;
+  return decode_workspace(sms, d) + (max_rows > kFewRows ? chunk_workspace(sms, d) : 0);
 }
 
 cudaError_t launch_attend_cache(const AttendArgs& a, int d, int code, int sms, cudaStream_t st) {
   const long long rows = static_cast<long long>(a.max_q < a.tokens ? a.max_q : a.tokens) * a.group;
-  if (rows <= kFewRows) return launch_decode(a, d, code, sms, 0x7fffffff, st);
-  // the two take turns with the workspace
-  const cudaError_t e = launch_decode(a, d, code, sms, kFewRows, st);
-  return e != cudaSuccess ? e : launch_chunk(a, d, code, sms, kFewRows, a.workspace, st);
+  const bool chunks = rows > kFewRows;
+  cudaError_t e = launch_decode(a, d, code, sms, chunks ? kFewRows : 0x7fffffff, st);
+  if (chunks && e == cudaSuccess) {
+    AttendArgs b = a;
+    b.workspace = static_cast<char*>(a.workspace) + decode_workspace(sms, d);
+    e = launch_chunk(b, d, code, sms, kFewRows, st);
+    if (e == cudaSuccess) e = launch_chunk_join(b, d, sms, st);
+  }
+  return e != cudaSuccess ? e : launch_decode_join(a, d, sms, st);
 }
 
 }  // namespace alhr

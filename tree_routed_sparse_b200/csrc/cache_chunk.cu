@@ -274,6 +274,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const uint32_t bars = smem + L::bars;
   auto bar = [&](int which, int i = 0) { return bars + (which + i) * 8; };
   volatile int* stop = reinterpret_cast<volatile int*>(chunk_smem + L::misc);
+  let_next_begin();
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(chunk_smem + L::misc + 16);
 
   // ---- the tile list
@@ -290,7 +291,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const long long end = piece < split.pieces ? split.first(piece + 1) : 0;
   JoinMeta* meta = space.meta + piece;
   if (tid == 0) meta->last = -1;
-  if (begin >= end) return;
+  if (begin >= end) {
+    wait_for_previous();
+    return;
+  }
   {
     const int c = chunk_of<kChunkThreads>(chunk_start, begin);
     long long at = chunk_start[c], head = 0;
@@ -360,26 +364,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       m = -INFINITY;
       l = 0.f;
       seen = 0x7fffffff;  // a row behind the last one masks nothing and is not written
-      float top = 0.f;
-      const bool on = row < cur.q.rows;
-      const uint4* p = nullptr;
-      if (on) {
+      uint4 raw[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) raw[c] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < cur.q.rows) {
         const int tok = row / a.group;
         seen = static_cast<int>(max(min(static_cast<long long>(cur.q.ctx) + tok + 1,
                                         static_cast<long long>(cur.q.see)), 0LL));
-        p = reinterpret_cast<const uint4*>(
+        const uint4* p = reinterpret_cast<const uint4*>(
             static_cast<const uint16_t*>(a.q) + (cur.q.q_lo + tok) * a.q_token_stride +
             (cur.h * a.group + (row - tok * a.group)) * a.q_head_stride);
-#pragma unroll 4
-        for (int c = 0; c < kCols; ++c) {
-          const uint4 w = __ldg(p + c);
-          float y[8];
-          if (a.fp16) unpack8<ALHR_TYPE_FP16>(w, w, y);
-          else unpack8<ALHR_TYPE_BF16>(w, w, y);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(y[j]));
-        }
+        for (int c = 0; c < kCols; ++c) raw[c] = __ldg(p + c);
       }
+      // magnitudes of both types order like their bits
+      uint32_t hi = 0;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        hi = __vmaxu2(hi, __vmaxu2(__vmaxu2(raw[c].x & 0x7fff7fffu, raw[c].y & 0x7fff7fffu),
+                                   __vmaxu2(raw[c].z & 0x7fff7fffu, raw[c].w & 0x7fff7fffu)));
+      }
+      hi = max(hi & 0xffffu, hi >> 16);
+      const float top = a.fp16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(hi)))
+                               : __uint_as_float(hi << 16);
       const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100), 126);
       // a negative factor of the scores goes into the queries: what follows takes the largest
       // score as the largest product
@@ -387,19 +394,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                                  a.scale_log2);
       qs = __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23) * fabsf(a.scale_log2);
       const uint32_t dst = smem + L::q + i * L::kTile + (rt >> 3) * (kCols * 128) + (rt & 7) * 16;
-#pragma unroll 2
+#pragma unroll
       for (int c = 0; c < kCols; ++c) {
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (on) {
-          w = __ldg(p + c);
-          float y[8];
-          if (a.fp16) unpack8<ALHR_TYPE_FP16>(w, w, y);
-          else unpack8<ALHR_TYPE_BF16>(w, w, y);
-          w = make_uint4(pack2(y[0] * up, y[1] * up, true), pack2(y[2] * up, y[3] * up, true),
-                         pack2(y[4] * up, y[5] * up, true), pack2(y[6] * up, y[7] * up, true));
-        }
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(dst + c * 128), "r"(w.x),
-                     "r"(w.y), "r"(w.z), "r"(w.w)
+        float y[8];
+        if (a.fp16) unpack8<ALHR_TYPE_FP16>(raw[c], raw[c], y);
+        else unpack8<ALHR_TYPE_BF16>(raw[c], raw[c], y);
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(dst + c * 128),
+                     "r"(pack2(y[0] * up, y[1] * up, true)), "r"(pack2(y[2] * up, y[3] * up, true)),
+                     "r"(pack2(y[4] * up, y[5] * up, true)), "r"(pack2(y[6] * up, y[7] * up, true))
                      : "memory");
       }
       fence_shared();
@@ -788,11 +790,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (warp == 8)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512)
                  : "memory");
+  wait_for_previous();  // what follows this kernel follows the one before it too
 }
 
 template <int D, int CODE>
-cudaError_t chunk_as(const AttendArgs& a, int sms, int row_limit, void* workspace,
-                     cudaStream_t st) {
+cudaError_t chunk_as(const AttendArgs& a, int sms, int row_limit, cudaStream_t st) {
   static thread_local bool configured[128] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -802,26 +804,29 @@ cudaError_t chunk_as(const AttendArgs& a, int sms, int row_limit, void* workspac
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 128) configured[dev] = true;
   }
-  JoinSpace space = join_space(workspace, sms);
-  chunk_kernel<D, CODE><<<sms, kChunkThreads, ChunkSmem<D>::bytes, st>>>(a, space, row_limit);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  join_kernel<D, kRows><<<dim3(sms, kRows / kJoinRows), kJoinRows * 32, 0, st>>>(a, space);
-  return cudaGetLastError();
+  return launch_behind(chunk_kernel<D, CODE>, dim3(sms), kChunkThreads, ChunkSmem<D>::bytes, st, a,
+                       join_space(a.workspace, sms), row_limit);
 }
 
 }  // namespace
 
 size_t chunk_workspace(int sms, int d) { return join_bytes(sms, kRows, d); }
 
-// Requests of more than row_limit rows (of one key head).
+// Requests of more than row_limit rows (of one key head); the join has to follow. The kernel may
+// run beside the previous one of the stream, whose results it does not read, and ends behind it.
 cudaError_t launch_chunk(const AttendArgs& a, int d, int code, int sms, int row_limit,
-                         void* workspace, cudaStream_t st) {
+                         cudaStream_t st) {
   if (d == 64)
-    return code == ALHR_CODE_INT8 ? chunk_as<64, ALHR_CODE_INT8>(a, sms, row_limit, workspace, st)
-                                  : chunk_as<64, ALHR_CODE_E4M3>(a, sms, row_limit, workspace, st);
-  return code == ALHR_CODE_INT8 ? chunk_as<128, ALHR_CODE_INT8>(a, sms, row_limit, workspace, st)
-                                : chunk_as<128, ALHR_CODE_E4M3>(a, sms, row_limit, workspace, st);
+    return code == ALHR_CODE_INT8 ? chunk_as<64, ALHR_CODE_INT8>(a, sms, row_limit, st)
+                                  : chunk_as<64, ALHR_CODE_E4M3>(a, sms, row_limit, st);
+  return code == ALHR_CODE_INT8 ? chunk_as<128, ALHR_CODE_INT8>(a, sms, row_limit, st)
+                                : chunk_as<128, ALHR_CODE_E4M3>(a, sms, row_limit, st);
+}
+
+cudaError_t launch_chunk_join(const AttendArgs& a, int d, int sms, cudaStream_t st) {
+  const JoinSpace space = join_space(a.workspace, sms);
+  return d == 64 ? launch_join<64, kRows>(a, space, sms, st)
+                 : launch_join<128, kRows>(a, space, sms, st);
 }
 
 }  // namespace alhr

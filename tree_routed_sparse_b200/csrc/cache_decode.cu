@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
+  let_next_begin();
 
   // ---- the tile list: every thread sums a run of requests
   const int per = (a.requests + kDecodeWarps * 32 - 1) / (kDecodeWarps * 32);
@@ -502,37 +503,45 @@ cudaError_t decode_as(const AttendArgs& a, int sms, int row_limit, cudaStream_t 
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 128) configured[dev] = true;
   }
-  const int pieces = sms * kDecodeWarps;
-  const JoinSpace space = join_space(a.workspace, pieces);
-  decode_kernel<D, CODE, NT><<<sms, kDecodeWarps * 32, kSmem, st>>>(a, space, row_limit);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  join_kernel<D, 8 * NT><<<dim3(pieces, NT), kJoinRows * 32, 0, st>>>(a, space);
+  decode_kernel<D, CODE, NT><<<sms, kDecodeWarps * 32, kSmem, st>>>(
+      a, join_space(a.workspace, sms * kDecodeWarps), row_limit);
   return cudaGetLastError();
+}
+
+template <int D, int CODE>
+cudaError_t decode_with(const AttendArgs& a, int sms, int row_limit, bool one, cudaStream_t st) {
+  return one ? decode_as<D, CODE, 1>(a, sms, row_limit, st)
+             : decode_as<D, CODE, 2>(a, sms, row_limit, st);
+}
+
+// Whether no request has more than eight rows, so that one column group of the product holds them.
+bool one_group(const AttendArgs& a) {
+  return static_cast<long long>(a.max_q < a.tokens ? a.max_q : a.tokens) * a.group <= 8;
 }
 
 }  // namespace
 
-size_t decode_workspace(int sms, int d) {
-  return join_bytes(sms * kDecodeWarps, 16, d);
-}
+size_t decode_workspace(int sms, int d) { return join_bytes(sms * kDecodeWarps, 16, d); }
 
-// Requests of at most row_limit rows (of one key head).
+// Requests of at most row_limit rows (of one key head); the join has to follow.
 cudaError_t launch_decode(const AttendArgs& a, int d, int code, int sms, int row_limit,
                           cudaStream_t st) {
-  const long long rows = static_cast<long long>(a.max_q < a.tokens ? a.max_q : a.tokens) * a.group;
-  const bool one = rows <= 8;
+  const bool one = one_group(a);
   if (d == 64)
-    return code == ALHR_CODE_INT8
-               ? (one ? decode_as<64, ALHR_CODE_INT8, 1>(a, sms, row_limit, st)
-                      : decode_as<64, ALHR_CODE_INT8, 2>(a, sms, row_limit, st))
-               : (one ? decode_as<64, ALHR_CODE_E4M3, 1>(a, sms, row_limit, st)
-                      : decode_as<64, ALHR_CODE_E4M3, 2>(a, sms, row_limit, st));
-  return code == ALHR_CODE_INT8
-             ? (one ? decode_as<128, ALHR_CODE_INT8, 1>(a, sms, row_limit, st)
-                    : decode_as<128, ALHR_CODE_INT8, 2>(a, sms, row_limit, st))
-             : (one ? decode_as<128, ALHR_CODE_E4M3, 1>(a, sms, row_limit, st)
-                    : decode_as<128, ALHR_CODE_E4M3, 2>(a, sms, row_limit, st));
+    return code == ALHR_CODE_INT8 ? decode_with<64, ALHR_CODE_INT8>(a, sms, row_limit, one, st)
+                                  : decode_with<64, ALHR_CODE_E4M3>(a, sms, row_limit, one, st);
+  return code == ALHR_CODE_INT8 ? decode_with<128, ALHR_CODE_INT8>(a, sms, row_limit, one, st)
+                                : decode_with<128, ALHR_CODE_E4M3>(a, sms, row_limit, one, st);
+}
+
+cudaError_t launch_decode_join(const AttendArgs& a, int d, int sms, cudaStream_t st) {
+  const int pieces = sms * kDecodeWarps;
+  const JoinSpace space = join_space(a.workspace, pieces);
+  if (one_group(a))
+    return d == 64 ? launch_join<64, 8>(a, space, pieces, st)
+                   : launch_join<128, 8>(a, space, pieces, st);
+  return d == 64 ? launch_join<64, 16>(a, space, pieces, st)
+                 : launch_join<128, 16>(a, space, pieces, st);
 }
 
 }  // namespace alhr

@@ -83,13 +83,15 @@ cudaError_t launch_plan_blocks(const PlanArgs& a, cudaStream_t st);
 cudaError_t launch_store_cache(const StoreArgs& a, int d, int code, int type, cudaStream_t st);
 cudaError_t launch_load_cache(const LoadArgs& a, int d, int code, int type, cudaStream_t st);
 size_t attend_cache_workspace(int sms, int d, long long max_rows);
+cudaError_t launch_attend_cache(const AttendArgs& a, int d, int code, int sms, cudaStream_t st);
 size_t decode_workspace(int sms, int d);
 cudaError_t launch_decode(const AttendArgs& a, int d, int code, int sms, int row_limit,
                           cudaStream_t st);
-cudaError_t launch_attend_cache(const AttendArgs& a, int d, int code, int sms, cudaStream_t st);
+cudaError_t launch_decode_join(const AttendArgs& a, int d, int sms, cudaStream_t st);
 size_t chunk_workspace(int sms, int d);
 cudaError_t launch_chunk(const AttendArgs& a, int d, int code, int sms, int row_limit,
-                         void* workspace, cudaStream_t st);
+                         cudaStream_t st);
+cudaError_t launch_chunk_join(const AttendArgs& a, int d, int sms, cudaStream_t st);
 cudaError_t launch_attend_selected(const SelectArgs& a, int d, int code, int sms, cudaStream_t st);
 
 }  // namespace alhr

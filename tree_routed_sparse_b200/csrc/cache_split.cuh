@@ -89,48 +89,128 @@ inline JoinSpace join_space(void* workspace, int pieces) {
                    reinterpret_cast<float*>(static_cast<char*>(workspace) + pieces * 32)};
 }
 
-constexpr int kJoinRows = 8;
+// The next kernel of the stream may be set up while this one runs (it waits before it reads what
+// this one writes).
+__device__ __forceinline__ void let_next_begin() {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+}
 
-// Joins the partial sums in the order of the pieces: grid (pieces, ROWS / kJoinRows), one warp a
-// row, weights 2^(M_i - max M).
+// Launches a kernel that waits for the previous one of the stream by itself.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                          cudaStream_t st, A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+constexpr int kJoinWarps = 8;
+
+// Joins the partial sums of the units that span pieces, one CTA (of ROWS / 16 along y) for each
+// piece in which such a unit begins. Up to eight warps share a row: each joins every k-th partial
+// (the lanes take 32 weights 2^(M_i - max M) at a time, so that the loads of the sums do not wait
+// for one another), then their sums are added in the order of the warps.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kJoinRows * 32) join_kernel(const AttendArgs a,
-                                                              const JoinSpace space) {
-  const int piece = blockIdx.x, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
-  const JoinMeta p = space.meta[piece];
-  if (p.last < 0 || row >= p.rows) return;
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendArgs a,
+                                                               const JoinSpace space) {
+  wait_for_previous();
   constexpr int E = D / 32, kStep = ROWS * (D + 2);
-  const int n = p.last - piece + 1;
+  const int piece = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const JoinMeta p = space.meta[piece];
+  const int row0 = blockIdx.y * 16;
+  const int rows = min(p.rows - row0, 16);
+  if (p.last < 0 || rows <= 0) return;
+  int shared_by = 1;  // warps of a row
+  while (rows * shared_by * 2 <= kJoinWarps) shared_by *= 2;
+  __shared__ float sums[kJoinWarps][D + 2];
+  const int n = p.last - piece + 1, sub = warp % shared_by;
+  // partials: slot 1 of this piece, slot 0 of the pieces behind it
   auto part = [&](int i) {
     return space.part + (static_cast<long long>(piece + i) * 2 + (i == 0 ? 1 : 0)) * kStep;
   };
-  float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, part(i)[ROWS * D + row]);
+  for (int r = warp / shared_by; r < rows; r += kJoinWarps / shared_by) {
+    const int row = row0 + r;
+    float m = -INFINITY;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, part(i)[ROWS * D + row]);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float base = m == -INFINITY ? 0.f : m;
-  float acc[E], l = 0.f;
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float base = m == -INFINITY ? 0.f : m;
+    float acc[E], l = 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* x = part(i);
-    const float f = exp2_fast(x[ROWS * D + row] - base);
-    l = fmaf(x[ROWS * D + ROWS + row], f, l);
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    const int mine = (n - sub + shared_by - 1) / shared_by;  // partials sub, sub + shared_by, ...
+    for (int i0 = 0; i0 < mine; i0 += 32) {
+      float f = 0.f;
+      if (i0 + lane < mine) {
+        const float* x = part(sub + (i0 + lane) * shared_by) + ROWS * D + row;
+        f = exp2_fast(x[0] - base);
+        l = fmaf(x[ROWS], f, l);
+      }
+      const int some = min(32, mine - i0);
+#pragma unroll 8
+      for (int i = 0; i < some; ++i) {
+        const float w = __shfl_sync(0xffffffffu, f, i);
+        const float* x = part(sub + (i0 + i) * shared_by) + row * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(x);
+          acc[0] = fmaf(y.x, w, acc[0]);
+          acc[1] = fmaf(y.y, w, acc[1]);
+          acc[2] = fmaf(y.z, w, acc[2]);
+          acc[3] = fmaf(y.w, w, acc[3]);
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(x);
+          acc[0] = fmaf(y.x, w, acc[0]);
+          acc[1] = fmaf(y.y, w, acc[1]);
+        }
+      }
+    }
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(x[row * D + lane * E + e], f, acc[e]);
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (shared_by > 1) {  // then every warp has one row at most, and all of them come here
+#pragma unroll
+      for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = acc[e];
+      if (lane == 0) sums[warp][D] = l;
+      // the warps of rows that there are
+      asm volatile("bar.sync 1, %0;\n" ::"r"(rows * shared_by * 32) : "memory");
+      if (sub == 0) {
+        for (int k = 1; k < shared_by; ++k) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += sums[warp + k][lane * E + e];
+          l += sums[warp + k][D];
+        }
+      }
+    }
+    if (sub == 0) {
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const int rr = p.row0 + row, tok = rr / a.group;
+      const int q_lo = min(max(__ldg(a.q_start + p.r), 0), a.tokens);
+      const long long at = static_cast<long long>(q_lo + tok) * a.q_heads + p.h * a.group +
+                           (rr - tok * a.group);
+#pragma unroll
+      for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at * D + lane * E + e) =
+            pack2(acc[e] * inv, acc[e + 1] * inv, a.fp16);
+      if (a.lse && lane == 0)
+        a.lse[at] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const int rr = p.row0 + row, tok = rr / a.group;
-  const int q_lo = min(max(__ldg(a.q_start + p.r), 0), a.tokens);
-  const long long at = static_cast<long long>(q_lo + tok) * a.q_heads + p.h * a.group +
-                       (rr - tok * a.group);
-#pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at * D + lane * E + e) =
-        pack2(acc[e] * inv, acc[e + 1] * inv, a.fp16);
-  if (a.lse && lane == 0) a.lse[at] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <int D, int ROWS>
+cudaError_t launch_join(const AttendArgs& a, const JoinSpace& space, int pieces, cudaStream_t st) {
+  return launch_behind(join_kernel<D, ROWS>, dim3(pieces, (ROWS + 15) / 16), kJoinWarps * 32, 0, st,
+                       a, space);
 }
 
 }  // namespace alhr
