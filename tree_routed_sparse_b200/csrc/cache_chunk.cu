@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         if (!done) {
           float top = -INFINITY;  // the largest x of the row
-#pragma unroll 1
+#pragma unroll 2
           for (int c = 0; c < 4; ++c) {
             uint32_t v[32];
             tmem_ld32(v, s_col + c * 32);
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
           }
           const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll 1
+#pragma unroll 2
           for (int c = 0; c < 4; ++c) {
             uint32_t v[32], p[16];
             tmem_ld32(v, s_col + c * 32);
