@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
   // ---- copies, kStages tiles ahead
   const uint32_t ring = shared_u32(decode_smem) + warp * (kStages * Tile<D>::kStride);
   const int crow = lane / LPR, cpiece = lane % LPR;
+  const uint32_t place0 = piece_offset<D>(crow, cpiece), place1 = piece_offset<D>(RPI + crow, cpiece);
   bool bad = false;
   // block of 16-key group `lane` of the loader's tile; -1: no visible key in it; -2: a bad number
   auto fetch_block = [&]() {
@@ -176,16 +177,25 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
       const int block = __shfl_sync(0xffffffffu, next_block, s);
       const int key0 = load.tile * Tile<D>::kKeys + s * 16;
       const int there = block >= 0 ? min(16, load.q.see - key0) : 0;  // rows of the group to copy
-      const long long row0 =
-          block_row(a.c, max(block, 0), load.h) + (key0 & (a.c.bs - 1));
+      const long long src = (block_row(a.c, max(block, 0), load.h) + (key0 & (a.c.bs - 1))) * D;
+      const uint8_t* const k = a.c.k + src + lane * 16;
+      const uint8_t* const v = a.c.v + src + lane * 16;
+      const uint32_t dst = base + s * 16 * D;
+      if (there == 16) {  // the same place a row group later, but for the order of the pieces
 #pragma unroll
-      for (int i = 0; i < 16 / RPI; ++i) {
-        const int row = i * RPI + crow;  // of the group
-        const int n = row < there ? 16 : 0;
-        const long long src = (row0 + (n ? row : 0)) * D + (n ? cpiece * 16 : 0);
-        const uint32_t dst = base + s * 16 * D + piece_offset<D>(row, cpiece);
-        copy16(dst, a.c.k + src, n);
-        copy16(dst + kStageBytes / 2, a.c.v + src, n);
+        for (int i = 0; i < 16 / RPI; ++i) {
+          const uint32_t at = dst + (i & 1 ? place1 : place0) + (i & ~1) * 512;
+          copy16(at, k + i * 512, 16);
+          copy16(at + kStageBytes / 2, v + i * 512, 16);
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < 16 / RPI; ++i) {
+          const int n = i * RPI + crow < there ? 16 : 0;
+          const uint32_t at = dst + (i & 1 ? place1 : place0) + (i & ~1) * 512;
+          copy16(at, n ? k + i * 512 : a.c.k, n);
+          copy16(at + kStageBytes / 2, n ? v + i * 512 : a.c.v, n);
+        }
       }
     }
     if (lane < SUBS) {
@@ -199,7 +209,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
     }
   };
   long long loaded = begin;
-#pragma unroll
+#pragma unroll 1
   for (int s = 0; s < kStages; ++s) {
     if (loaded < end) {
       issue(s);
@@ -391,7 +401,6 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
     }
     // M moves only when it has to: the largest weight is between 2^7 and 2^15
     bool grow = false;
-    float top[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -399,15 +408,17 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
         float x = fmaxf(s[0][n][c], s[0][n][2 + c]);
 #pragma unroll
         for (int u = 1; u < SUBS; ++u) x = fmaxf(x, fmaxf(s[u][n][c], s[u][n][2 + c]));
-        top[n][c] = group_max(x);
-        grow |= top[n][c] > m[n][c] + kTopLog + 8.f;
+        grow |= x > m[n][c] + kTopLog + 8.f;
       }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float mn = fmaxf(m[n][c], top[n][c] - kTopLog);
+          float x = fmaxf(s[0][n][c], s[0][n][2 + c]);
+#pragma unroll
+          for (int u = 1; u < SUBS; ++u) x = fmaxf(x, fmaxf(s[u][n][c], s[u][n][2 + c]));
+          const float mn = fmaxf(m[n][c], group_max(x) - kTopLog);
           const float keep = mn == -INFINITY ? 1.f : exp2_fast(m[n][c] - mn);
           m[n][c] = mn;
           l[n][c] *= keep;
