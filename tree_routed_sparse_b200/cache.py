@@ -146,11 +146,10 @@ def plan_blocks(ctx_len: torch.Tensor, new_len: torch.Tensor, block_table: torch
     table = _need(block_table, torch.int32, (r, width), "block_table", dev)
     free = _need(free_blocks, torch.int32, free_blocks.shape, "free_blocks", dev)
     first = _need(free_first, torch.int32, (1,), "free_first", dev)
-    q_start = ctx_len.new_empty(r + 1)
-    seq_len = ctx_len.new_empty(r)
     slots = ctx_len.new_empty(tokens, dtype=torch.int64)
-    positions = ctx_len.new_empty(tokens)
-    free_next = ctx_len.new_empty(1)
+    # one allocation for what is 32 bits wide
+    q_start, seq_len, positions, free_next = ctx_len.new_empty(2 * r + tokens + 2).split(
+        (r + 1, r, tokens, 1))
     _call("alhr_plan_blocks", dev, r, width, block_size, min(blocks, (2**31 - 1) // block_size),
           tokens, free_blocks.numel(), ctx, new, table, free, first, q_start.data_ptr(),
           seq_len.data_ptr(), slots.data_ptr(), positions.data_ptr(), free_next.data_ptr(),
@@ -261,9 +260,9 @@ def attend_cache(Q: torch.Tensor, cache: dict, block_table: torch.Tensor, ctx_le
 
 def _workspace(cp, qp, dev) -> int:
     if _current_device() == dev.index:
-        return max(16, alhr.lib().alhr_attend_cache_workspace(cp, qp))
+        return alhr.lib().alhr_attend_cache_workspace(cp, qp)
     with torch.cuda.device(dev):
-        return max(16, alhr.lib().alhr_attend_cache_workspace(cp, qp))
+        return alhr.lib().alhr_attend_cache_workspace(cp, qp)
 
 
 def attend_cache_workspace(Q: torch.Tensor, cache: dict, block_table: torch.Tensor) -> int:

@@ -22,13 +22,13 @@ constexpr int kSelWarps = 4;
 constexpr int kSelKeys = 96, kSelGroups = kSelKeys / 16;
 
 struct SelKey {
-  int row;        // code row of the key's head, -1: skipped
+  int row;        // code row of the key's head; of another key of the query where this one is skipped
+  int on;         // 0: skipped
   float k_scale, v_scale;
-  int pad;
 };
 
 template <int D, int CODE>
-__global__ void __launch_bounds__(kSelWarps * 32, 4) selected_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kSelWarps * 32, D == 64 ? 8 : 6) selected_kernel(const SelectArgs a) {
   constexpr int KS = D / 16;   // products over d of one 16-key group
   constexpr int W = D / 32;    // words of values a lane takes of a key
   __shared__ SelKey keys[kSelWarps][kSelKeys];
@@ -37,8 +37,8 @@ __global__ void __launch_bounds__(kSelWarps * 32, 4) selected_kernel(const Selec
   SelKey* const mine = keys[warp];
   for (long long u = static_cast<long long>(blockIdx.x) * kSelWarps + warp; u < a.rows;
        u += static_cast<long long>(gridDim.x) * kSelWarps) {
-    const int bh = static_cast<int>(u / a.nq);
-    const int row_t = static_cast<int>(u - static_cast<long long>(bh) * a.nq);
+    const int bh = static_cast<int>(u) / a.nq;  // rows are below 2^31
+    const int row_t = static_cast<int>(u) - bh * a.nq;
     const int b = bh / a.q_heads, h = (bh - b * a.q_heads) / a.group;
     const int count = min(max(__ldg(a.count + u), 0), a.max_keys);
     const long long cap = static_cast<long long>(a.max_blocks) << a.c.bs_log;
@@ -46,10 +46,11 @@ __global__ void __launch_bounds__(kSelWarps * 32, 4) selected_kernel(const Selec
     const long long see = min(min(pos + 1, static_cast<long long>(__ldg(a.seq_len + b))), cap);
     // ---- where the keys lie
     uint32_t flags = 0;
+    int spare = 0;
 #pragma unroll
     for (int i = 0; i < kSelKeys / 32; ++i) {
       const int e = i * 32 + lane;
-      SelKey k{-1, 0.f, 0.f, 0};
+      SelKey k{-1, 0, 0.f, 0.f};
       if (e < count) {
         const int j = __ldg(a.idx + u * a.max_keys + e);
         if (j >= 0 && j < see) {
@@ -58,6 +59,7 @@ __global__ void __launch_bounds__(kSelWarps * 32, 4) selected_kernel(const Selec
           if (block >= 0 && block < a.c.blocks) {
             const long long si = static_cast<long long>(block) * a.c.heads + h;
             k.row = static_cast<int>((si << a.c.bs_log) + (j & (a.c.bs - 1)));
+            k.on = 1;
             k.k_scale = __ldg(a.c.k_scale + si);
             k.v_scale = __ldg(a.c.v_scale + si);
           } else {
@@ -67,47 +69,55 @@ __global__ void __launch_bounds__(kSelWarps * 32, 4) selected_kernel(const Selec
           flags |= ALHR_DEVERR_INDEX;
         }
       }
+      // a skipped key reads the row of one that is not (in bounds, and as finite as the rest)
+      const unsigned some = __ballot_sync(0xffffffffu, k.on);
+      if (some) spare = __shfl_sync(0xffffffffu, k.row, __ffs(some) - 1);
+      if (!k.on) k.row = spare;
       mine[e] = k;
     }
     flags = __reduce_or_sync(0xffffffffu, flags);
     if (flags && lane == 0) cache_flag(a.dev_err, flags);
     // ---- the query: lane t holds numbers 16 (4 j + t) .. + 15, scaled by a power of two
-    float x[D / 4];
-    float top = 0.f;
+    uint32_t qf[KS][2];
+    float qs;
+    {
+      float x[D / 4];
+      float top = 0.f;
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
-      const long long at = u * D + (j * 4 + t) * 16;
-      if (a.type == ALHR_TYPE_INT8) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const int8_t*>(a.q) + at));
-        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+      for (int j = 0; j < D / 64; ++j) {
+        const long long at = u * D + (j * 4 + t) * 16;
+        if (a.type == ALHR_TYPE_INT8) {
+          const uint4 w =
+              __ldg(reinterpret_cast<const uint4*>(static_cast<const int8_t*>(a.q) + at));
+          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          x[j * 16 + i] = static_cast<float>(static_cast<int8_t>(v[i >> 2] >> (8 * (i & 3))));
-      } else {
-        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
+          for (int i = 0; i < 16; ++i)
+            x[j * 16 + i] = static_cast<float>(static_cast<int8_t>(v[i >> 2] >> (8 * (i & 3))));
+        } else {
+          const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 w = __ldg(p + i);
-          float y[8];
-          if (a.type == ALHR_TYPE_FP16) unpack8<ALHR_TYPE_FP16>(w, w, y);
-          else unpack8<ALHR_TYPE_BF16>(w, w, y);
+          for (int i = 0; i < 2; ++i) {
+            const uint4 w = __ldg(p + i);
+            float y[8];
+            if (a.type == ALHR_TYPE_FP16) unpack8<ALHR_TYPE_FP16>(w, w, y);
+            else unpack8<ALHR_TYPE_BF16>(w, w, y);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) x[j * 16 + i * 8 + c] = y[c];
+            for (int c = 0; c < 8; ++c) x[j * 16 + i * 8 + c] = y[c];
+          }
         }
       }
-    }
 #pragma unroll
-    for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const int e2 = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100), 126);
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e2) << 23);
-    const float qs = __uint_as_float(static_cast<uint32_t>(127 - 14 + e2) << 23) * a.scale_log2;
-    uint32_t qf[KS][2];
+      for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e2 = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100), 126);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e2) << 23);
+      qs = __uint_as_float(static_cast<uint32_t>(127 - 14 + e2) << 23) * a.scale_log2;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      qf[s][0] = pack2(x[4 * s] * up, x[4 * s + 1] * up, true);
-      qf[s][1] = pack2(x[4 * s + 2] * up, x[4 * s + 3] * up, true);
+      for (int s = 0; s < KS; ++s) {
+        qf[s][0] = pack2(x[4 * s] * up, x[4 * s + 1] * up, true);
+        qf[s][1] = pack2(x[4 * s + 2] * up, x[4 * s + 3] * up, true);
+      }
     }
     __syncwarp();
     // ---- scores of keys 16 i + g and 16 i + 8 + g
@@ -122,12 +132,10 @@ __global__ void __launch_bounds__(kSelWarps * 32, 4) selected_kernel(const Selec
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
           const int piece = (j * 4 + t) * 16;
-          w0[j] = k0.row >= 0 ? __ldg(reinterpret_cast<const uint4*>(
-                                    a.c.k + static_cast<long long>(k0.row) * D + piece))
-                              : make_uint4(0u, 0u, 0u, 0u);
-          w1[j] = k1.row >= 0 ? __ldg(reinterpret_cast<const uint4*>(
-                                    a.c.k + static_cast<long long>(k1.row) * D + piece))
-                              : make_uint4(0u, 0u, 0u, 0u);
+          w0[j] = __ldg(reinterpret_cast<const uint4*>(
+              a.c.k + static_cast<long long>(k0.row) * D + piece));
+          w1[j] = __ldg(reinterpret_cast<const uint4*>(
+              a.c.k + static_cast<long long>(k1.row) * D + piece));
         }
         float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -142,8 +150,8 @@ __global__ void __launch_bounds__(kSelWarps * 32, 4) selected_kernel(const Selec
             mma16816(c, a0, a1, a2, a3, qf[j * 4 + k][0], qf[j * 4 + k][1]);
           }
         }
-        if (k0.row >= 0) s[i][0] = c[0] * (qs * k0.k_scale);
-        if (k1.row >= 0) s[i][1] = c[2] * (qs * k1.k_scale);
+        if (k0.on) s[i][0] = c[0] * (qs * k0.k_scale);
+        if (k1.on) s[i][1] = c[2] * (qs * k1.k_scale);
       }
     }
     // ---- weights
@@ -191,13 +199,12 @@ __global__ void __launch_bounds__(kSelWarps * 32, 4) selected_kernel(const Selec
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int row = mine[i * 16 + 2 * t + (r & 1) + (r >> 1) * 8].row;
-          const uint8_t* p = a.c.v + static_cast<long long>(max(row, 0)) * D + g * (D / 8);
+          const uint8_t* p = a.c.v + static_cast<long long>(row) * D + g * (D / 8);
           if constexpr (D == 128) {
-            const uint4 w = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(p))
-                                     : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
             v[r][0] = w.x; v[r][1] = w.y; v[r][2] = w.z; v[r][3] = w.w;
           } else {
-            const uint2 w = row >= 0 ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0u, 0u);
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
             v[r][0] = w.x; v[r][1] = w.y;
           }
         }
@@ -218,9 +225,10 @@ __global__ void __launch_bounds__(kSelWarps * 32, 4) selected_kernel(const Selec
     float* out = a.out + u * D + g * (D / 8);
 #pragma unroll
     for (int k = 0; k < KS / 2; ++k) {
-      const float4 y = make_float4((o[2 * k][0] + o[2 * k][1]) * inv, (o[2 * k][2] + o[2 * k][3]) * inv,
-                                   (o[2 * k + 1][0] + o[2 * k + 1][1]) * inv,
-                                   (o[2 * k + 1][2] + o[2 * k + 1][3]) * inv);
+      float4 y = make_float4((o[2 * k][0] + o[2 * k][1]) * inv, (o[2 * k][2] + o[2 * k][3]) * inv,
+                             (o[2 * k + 1][0] + o[2 * k + 1][1]) * inv,
+                             (o[2 * k + 1][2] + o[2 * k + 1][3]) * inv);
+      if (!(l > 0.f)) y = make_float4(0.f, 0.f, 0.f, 0.f);  // no key
       if (t == k) reinterpret_cast<float4*>(out)[k] = y;
     }
     __syncwarp();  // every lane has read the keys

@@ -82,7 +82,7 @@ __device__ __forceinline__ void decode4(uint32_t w, float* x) {
 
 // per: tokens a warp looks through for the beginnings of runs.
 template <int D, int CODE, int T>
-__global__ void __launch_bounds__(kStoreWarps * 32) store_kernel(const StoreArgs a, const int per) {
+__global__ void __launch_bounds__(kStoreWarps * 32, 6) store_kernel(const StoreArgs a, const int per) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes a row, rows a pass
   constexpr float kFull = CODE == ALHR_CODE_INT8 ? 127.f : 256.f;
   const int lane = threadIdx.x & 31;
@@ -98,15 +98,18 @@ __global__ void __launch_bounds__(kStoreWarps * 32) store_kernel(const StoreArgs
   const long long t0 = static_cast<long long>(blockIdx.x) * per;
   const int look = static_cast<int>(min(static_cast<long long>(per), a.tokens - t0));
 
-  // lane i: does a run begin at token t0 + i
+  // lane i: the slot of token t0 + i, and whether a run begins there (one of the first `look`)
   long long slot = -1;
   bool leads = false;
+  if (t0 + lane < a.tokens) slot = __ldg(a.slots + t0 + lane);
+  const long long before = t0 > 0 ? __ldg(a.slots + t0 - 1) : -1;  // the same for every lane
+  const long long above = __shfl_up_sync(0xffffffffu, slot, 1);
   if (lane < look) {
-    slot = __ldg(a.slots + t0 + lane);
     if (slot < 0 || slot >= slots_end) {
       if (slot != -1) cache_flag(a.dev_err, ALHR_DEVERR_BLOCK);
     } else {
-      leads = (slot & (bs - 1)) == 0 || t0 + lane == 0 || __ldg(a.slots + t0 + lane - 1) + 1 != slot;
+      const long long prev = lane ? above : before;
+      leads = (slot & (bs - 1)) == 0 || t0 + lane == 0 || prev + 1 != slot;
     }
   }
   for (unsigned left = __ballot_sync(0xffffffffu, leads); left; left &= left - 1) {
@@ -114,13 +117,18 @@ __global__ void __launch_bounds__(kStoreWarps * 32) store_kernel(const StoreArgs
     const long long s0 = __shfl_sync(0xffffffffu, slot, at);
     const long long t = t0 + at;
     const int off = static_cast<int>(s0 & (bs - 1));
-    int n = 0;  // rows of the run
     const int most = static_cast<int>(min(static_cast<long long>(bs - off), a.tokens - t));
-    for (int i = 0; i < most; i += 32) {
-      const bool on = i + lane < most && __ldg(a.slots + t + i + lane) == s0 + i + lane;
-      const unsigned m = __ballot_sync(0xffffffffu, on);
-      n += m == 0xffffffffu ? 32 : __ffs(~m) - 1;
-      if (m != 0xffffffffu) break;
+    // rows of the run: those among the lanes' tokens, then further ones
+    const unsigned here =
+        __ballot_sync(0xffffffffu, lane >= at && lane - at < most && slot == s0 + (lane - at)) >> at;
+    int n = here == 0xffffffffu ? 32 : __ffs(~here) - 1;
+    if (at + n == 32) {
+      for (int i = n; i < most; i += 32) {
+        const bool on = i + lane < most && __ldg(a.slots + t + i + lane) == s0 + i + lane;
+        const unsigned m = __ballot_sync(0xffffffffu, on);
+        n += m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+        if (m != 0xffffffffu) break;
+      }
     }
     const int block = static_cast<int>(s0 >> a.c.bs_log);
     const long long x0 = t * step + static_cast<long long>(h) * a.head_stride[which] + sub * 8;
@@ -203,52 +211,64 @@ __global__ void __launch_bounds__(kStoreWarps * 32) store_kernel(const StoreArgs
   }
 }
 
-// Threads (piece, token): 16 numbers of one head of one token, keys or values.
+// Threads (piece, token): eight numbers of one head, keys or values, of kTokens tokens each, whose
+// loads do not wait for one another.
+constexpr int kTokens = 4;
+
 template <int D, int CODE, int T>
 __global__ void __launch_bounds__(256) load_kernel(const LoadArgs a) {
-  constexpr int kPieces = D / 16;
+  constexpr int kPieces = D / 8;
   const int heads = a.c.heads, all = 2 * heads * kPieces;
   const long long slots_end = static_cast<long long>(a.c.blocks) << a.c.bs_log;
-  const int t = blockIdx.x * blockDim.y + threadIdx.y;
-  if (t >= a.tokens) return;
-  const long long slot = __ldg(a.slots + t);
-  const bool there = slot >= 0 && slot < slots_end;
-  if (!there && slot != -1 && threadIdx.x == 0) cache_flag(a.dev_err, ALHR_DEVERR_BLOCK);
-  const int block = there ? static_cast<int>(slot >> a.c.bs_log) : 0;
-  const int off = there ? static_cast<int>(slot & (a.c.bs - 1)) : 0;
-  for (int i = threadIdx.x; i < all; i += blockDim.x) {
-    const int sub = i % kPieces, hw = i / kPieces;
-    const int which = hw >= heads, h = hw - which * heads;
-    float v[16];
-    if (there) {
-      const uint8_t* codes =
-          (which ? a.c.v : a.c.k) + (block_row(a.c, block, h) + off) * D + sub * 16;
-      const float s =
-          __ldg((which ? a.c.v_scale : a.c.k_scale) + static_cast<long long>(block) * heads + h);
-      const uint4 c = __ldg(reinterpret_cast<const uint4*>(codes));
-      decode4<CODE>(c.x, v);
-      decode4<CODE>(c.y, v + 4);
-      decode4<CODE>(c.z, v + 8);
-      decode4<CODE>(c.w, v + 12);
+  const long long t0 = (static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y) * kTokens;
+  long long slot[kTokens];
+  bool bad = false;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = __fmul_rn(v[j], s);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = 0.f;
+  for (int i = 0; i < kTokens; ++i) {
+    slot[i] = t0 + i < a.tokens ? __ldg(a.slots + t0 + i) : -1;
+    if (slot[i] < 0 || slot[i] >= slots_end) {
+      bad |= slot[i] != -1;
+      slot[i] = -1;
     }
-    const long long at = (static_cast<long long>(t) * heads + h) * D + sub * 16;
-    if constexpr (T == ALHR_TYPE_FP32) {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.x[which]) + at);
+  }
+  if (bad && threadIdx.x == 0) cache_flag(a.dev_err, ALHR_DEVERR_BLOCK);
+  for (int p = threadIdx.x; p < all; p += blockDim.x) {
+    const int sub = p % kPieces, hw = p / kPieces;
+    const int which = hw >= heads, h = hw - which * heads;
+    const uint8_t* const codes = (which ? a.c.v : a.c.k) + sub * 8;
+    const float* const scales = (which ? a.c.v_scale : a.c.k_scale) + h;
+    uint2 c[kTokens];
+    float s[kTokens];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    } else {
-      constexpr bool kHalf = T == ALHR_TYPE_FP16;
-      uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.x[which]) + at);
+    for (int i = 0; i < kTokens; ++i) {
+      c[i] = make_uint2(0u, 0u);
+      s[i] = 0.f;
+      if (slot[i] >= 0) {
+        const int block = static_cast<int>(slot[i] >> a.c.bs_log);
+        const int off = static_cast<int>(slot[i] & (a.c.bs - 1));
+        c[i] = __ldg(reinterpret_cast<const uint2*>(codes + (block_row(a.c, block, h) + off) * D));
+        s[i] = __ldg(scales + static_cast<long long>(block) * heads);
+      }
+    }
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        p[j] = make_uint4(pack2(v[8 * j], v[8 * j + 1], kHalf), pack2(v[8 * j + 2], v[8 * j + 3], kHalf),
-                          pack2(v[8 * j + 4], v[8 * j + 5], kHalf),
-                          pack2(v[8 * j + 6], v[8 * j + 7], kHalf));
+    for (int i = 0; i < kTokens; ++i) {
+      if (t0 + i >= a.tokens) break;
+      float v[8];
+      decode4<CODE>(c[i].x, v);
+      decode4<CODE>(c[i].y, v + 4);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = slot[i] >= 0 ? __fmul_rn(v[j], s[i]) : 0.f;
+      const long long at = ((t0 + i) * heads + h) * D + sub * 8;
+      if constexpr (T == ALHR_TYPE_FP32) {
+        float4* q = reinterpret_cast<float4*>(static_cast<float*>(a.x[which]) + at);
+        q[0] = make_float4(v[0], v[1], v[2], v[3]);
+        q[1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+        constexpr bool kHalf = T == ALHR_TYPE_FP16;
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.x[which]) + at) =
+            make_uint4(pack2(v[0], v[1], kHalf), pack2(v[2], v[3], kHalf), pack2(v[4], v[5], kHalf),
+                       pack2(v[6], v[7], kHalf));
+      }
     }
   }
 }
@@ -267,11 +287,12 @@ cudaError_t store_as(const StoreArgs& a, cudaStream_t st) {
 
 template <int D, int CODE, int T>
 cudaError_t load_as(const LoadArgs& a, cudaStream_t st) {
-  const int pieces = 2 * a.c.heads * (D / 16);
+  const int pieces = 2 * a.c.heads * (D / 8);
   unsigned x = 32;
   while (x < 256 && x < static_cast<unsigned>(pieces)) x *= 2;
   const dim3 threads(x, 256 / x);
-  const unsigned grid = (static_cast<unsigned>(a.tokens) + threads.y - 1) / threads.y;
+  const unsigned each = threads.y * kTokens;
+  const unsigned grid = (static_cast<unsigned>(a.tokens) + each - 1) / each;
   load_kernel<D, CODE, T><<<grid, threads, 0, st>>>(a);
   return cudaGetLastError();
 }
