@@ -12,10 +12,10 @@
  *   alhr_attend_cache           softmax attention over all visible keys of each request
  *   alhr_attend_cache_selected  the same over selected positions, e.g. those of alhr_route
  *
- * Cache layout (row-major, contiguous, device memory, 16-byte aligned base pointers):
+ * Cache layout (row-major, contiguous, device memory; codes 16-byte, scales 4-byte aligned):
  *   k, v             8-bit codes [blocks][heads][block_size][d]
  *   k_scale, v_scale float       [blocks][heads]
- *   A key or value is code * scale of its block and head. Codes are int8 in [-127, 127] or e4m3
+ *   A key or value is code * scale of its block and head; scales are not negative. Codes are int8 in [-127, 127] or e4m3
  *   (4 exponent bits, 3 mantissa bits, no infinities).
  * A slot is block * block_size + offset (64 bits). Position p of request r lies in block
  * block_table[r][p / block_size] at offset p % block_size.
@@ -56,7 +56,7 @@ typedef struct {
   float* k_scale;
   float* v_scale;
   int32_t blocks;     /* >= 1; blocks * heads * block_size < 2^31 (else ALHR_ERR_UNSUPPORTED) */
-  int32_t heads;      /* key/value heads, >= 1                                                */
+  int32_t heads;      /* key/value heads, 1 to 65535 (more: ALHR_ERR_UNSUPPORTED)             */
   int32_t block_size; /* 16, 32, 64 or 128 tokens                                             */
   int32_t d;          /* 64 or 128                                                            */
   int32_t code;       /* an alhr_code                                                         */
@@ -79,11 +79,12 @@ typedef struct {
  * max_blocks * bs tokens, the free list ends, or there are more than `tokens` token rows (then
  * q_start stops at `tokens`). Negative lengths count as zero; a block number outside
  * [0, blocks) gives slot -1 and sets ALHR_DEVERR_BLOCK.
- *   requests     0 <= requests <= 8192 (more: ALHR_ERR_UNSUPPORTED)
+ *   requests     0 <= requests <= 8192; max_blocks * block_size <= 2^30 (else
+ *                ALHR_ERR_UNSUPPORTED)
  *   tokens       length of slots and positions, >= 0
  *   free_count   length of free_blocks, >= 0
  *   block_table  device int32 [requests][max_blocks], updated in place
- *   free_next may be free_first itself.
+ *   free_next is not free_first, seq_len neither ctx_len nor new_len (ALHR_ERR_INVALID_ARG).
  */
 ALHR_API alhr_status alhr_plan_blocks(int32_t requests, int32_t max_blocks, int32_t block_size,
                                       int32_t blocks, int32_t tokens, int32_t free_count,
@@ -136,7 +137,7 @@ typedef struct {
   int32_t tokens;         /* rows of Q and out, >= 0; tokens * q_heads < 2^31                  */
   int32_t q_heads;        /* a multiple of the cache's heads; query head h reads key head
                              h / (q_heads / heads); the quotient is at most 64                 */
-  int32_t max_blocks;     /* columns of block_table, >= 1; max_blocks * block_size < 2^31      */
+  int32_t max_blocks;     /* columns of block_table, >= 1; max_blocks * block_size <= 2^30     */
   int32_t max_q;          /* no request has more rows than this: it chooses the kernels, and
                              is no bound on what they compute; 0 means `tokens`                */
   int32_t type;           /* of Q and out: ALHR_TYPE_BF16 or ALHR_TYPE_FP16                    */
@@ -180,7 +181,7 @@ typedef struct {
   int32_t q_heads;    /* a multiple of the cache's heads, as above                             */
   int32_t nq;         /* query rows of each (b,h), >= 0; batch * q_heads * nq < 2^31           */
   int32_t max_keys;   /* columns of idx, 1 <= max_keys <= 96                                   */
-  int32_t max_blocks; /* columns of block_table, >= 1                                          */
+  int32_t max_blocks; /* columns of block_table, >= 1; max_blocks * block_size <= 2^30         */
   int32_t type;       /* of Q: ALHR_TYPE_INT8, BF16 or FP16                                    */
   float scale;        /* of the scores; finite                                                 */
 } alhr_cache_selection;

@@ -29,11 +29,11 @@ BAD_CACHES = [
     (dict(blocks=0), INVALID), (dict(heads=0), INVALID), (dict(code=2), INVALID),
     (dict(code=-1), INVALID), (dict(block_size=8), UNSUPPORTED), (dict(block_size=48), UNSUPPORTED),
     (dict(block_size=256), UNSUPPORTED), (dict(d=96), UNSUPPORTED), (dict(d=256), UNSUPPORTED),
-    (dict(blocks=1 << 27, heads=1, block_size=16), UNSUPPORTED),
+    (dict(blocks=1 << 27, heads=1, block_size=16), UNSUPPORTED), (dict(heads=65536), UNSUPPORTED),
     (dict(blocks=2 ** 31 - 1, heads=2 ** 31 - 1), UNSUPPORTED),
 ]
 BAD_MEMORY = [dict(k=None), dict(v=None), dict(k_scale=None), dict(v_scale=None), dict(k=P + 8),
-              dict(v=P + 1), dict(k_scale=P + 4), dict(v_scale=P + 8)]
+              dict(v=P + 1), dict(k_scale=P + 2), dict(v_scale=P + 1)]
 
 
 def test_plan_refusals(C):
@@ -42,17 +42,20 @@ def test_plan_refusals(C):
 
     def call(**kw):
         a = dict(requests=2, max_blocks=4, block_size=16, blocks=9, tokens=5, free_count=3, ctx=P,
-                 new=P, table=P, free=P, first=P, q_start=P, seq=P, slots=P, positions=P, nxt=P)
+                 new=P, table=P, free=P, first=P, q_start=P, seq=2 * P, slots=P, positions=P,
+                 nxt=2 * P)
         a.update(kw)
         return L.alhr_plan_blocks(*a.values(), None, None)
 
     for kw in (dict(requests=-1), dict(max_blocks=0), dict(blocks=0), dict(tokens=-1),
                dict(free_count=-1), dict(ctx=None), dict(new=None), dict(table=None),
                dict(free=None), dict(first=None), dict(q_start=None), dict(seq=None),
-               dict(slots=None), dict(positions=None), dict(nxt=None)):
+               dict(slots=None), dict(positions=None), dict(nxt=None),
+               # outputs that are inputs: CTAs would read what others have written
+               dict(nxt=P), dict(seq=P), dict(ctx=2 * P, seq=2 * P)):
         assert call(**kw) == INVALID, kw
     for kw in (dict(block_size=0), dict(block_size=24), dict(requests=8193),
-               dict(max_blocks=1 << 27)):
+               dict(max_blocks=1 << 27), dict(max_blocks=(1 << 26) + 1)):
         assert call(**kw) == UNSUPPORTED, kw
 
 
@@ -110,7 +113,7 @@ def test_attend_refusals(C):
                dict(scale=math.inf), dict(scale=3.4e38)):
         assert call(**kw) == INVALID, kw
     for kw in (dict(requests=8193), dict(q_heads=130), dict(tokens=1 << 30),
-               dict(max_blocks=1 << 27)):
+               dict(max_blocks=1 << 27), dict(max_blocks=(1 << 26) + 1)):
         assert call(**kw) == UNSUPPORTED, kw
     for k in ("Q", "table", "ctx", "seq", "start", "out", "ws"):
         assert call(ptrs={k: None}) == INVALID, k
@@ -174,6 +177,8 @@ def test_binding_refuses_what_it_cannot_pass_on(C):
         C._struct(c, torch.device("meta"))
     x = torch.zeros(4, 3, 2, 64)
     assert C._rows(x[:, 1], (4, 2, 64), torch.float32, "K", cpu) == (384, 64)
+    one = torch.zeros(67)[3:].as_strided((1, 1, 64), (5, 7, 1))
+    assert C._rows(one, (1, 1, 64), torch.float32, "K", cpu) == (0, 0)  # strides of nothing
     for bad in (x[:, 1].transpose(1, 2), x[:, 1, :, ::2], x[0, 1]):
         with pytest.raises(ValueError, match="K: expected"):
             C._rows(bad, (4, 2, 64), torch.float32, "K", cpu)

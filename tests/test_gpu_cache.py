@@ -366,6 +366,21 @@ def test_attend_blocks_outside_are_left_out(C, new):
     check(C, s, err_want=C.DEVERR_BLOCK)
 
 
+@pytest.mark.parametrize("new", [[1, 1, 1], [40, 30, 20]])
+def test_attend_lengths_and_offsets_out_of_range(C, new):
+    """Lengths up to the type's largest are cut at the table, offsets at the rows."""
+    s = make([100, 90, 50], new, 4, 2, 64, 16, I8, torch.bfloat16)
+    width, blocks = s["table"].shape[1], s["cache"]["k"].shape[0]
+    s["table"] %= blocks  # every entry is a block, so that a request may see the whole row
+    top = 2 ** 31 - 1
+    s["ctx"] = ints([top, top - 5, -2 ** 31])
+    s["seq"] = ints([top, 16 * width, top])
+    check(C, s)
+    s["ctx"], s["seq"] = ints([100, 90, 50]), ints([top, -4, 16 * width + 1])
+    s["start"][0], s["start"][3] = -7, top
+    check(C, s)
+
+
 @pytest.mark.parametrize("new", [[1, 1], [70, 130]])
 @pytest.mark.parametrize("code", [I8, E4])
 def test_attend_scales_far_apart(C, new, code):
@@ -454,6 +469,34 @@ def test_attend_two_streams_at_once(C):
                 got.append(run(x))
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_attend_refuses_what_it_cannot_use(C):
+    from tree_routed_sparse_b200 import alhr
+    s = make([10], [1], 4, 2, 64, 16, I8, torch.bfloat16)
+    call = lambda **kw: C.attend_cache(*[dict(s, **kw)[k] for k in (
+        "q", "cache", "table", "ctx", "seq", "start")], **{k: v for k, v in kw.items() if k in (
+            "out", "workspace", "max_q", "scale")})
+    with pytest.raises(ValueError, match="block_table"):
+        call(table=s["table"].cpu())
+    with pytest.raises(ValueError, match="q_start"):
+        call(start=s["start"][:1])
+    with pytest.raises(ValueError, match="Q"):
+        call(q=s["q"].float())
+    with pytest.raises(ValueError, match="Q"):
+        call(q=torch.cat([s["q"], s["q"]], -1)[..., ::2])
+    with pytest.raises(ValueError, match="out"):
+        call(out=torch.empty(1, 4, 64, device="cuda"))
+    with pytest.raises(ValueError, match="max_q"):
+        call(max_q=0)
+    with pytest.raises(alhr.AlhrError, match="INVALID_ARG"):
+        call(workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(alhr.AlhrError, match="INVALID_ARG"):
+        call(scale=math.inf)
+    with pytest.raises(alhr.AlhrError, match="INVALID_ARG"):
+        call(q=s["q"][:, :3].contiguous())
+    with pytest.raises(alhr.AlhrError, match="INVALID_ARG"):  # rows of an odd distance
+        call(q=torch.empty(3, 4, 67, dtype=torch.bfloat16, device="cuda")[:1, :, :64])
 
 
 # ------------------------------------------------------------------ selected keys

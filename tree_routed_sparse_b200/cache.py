@@ -165,7 +165,8 @@ def _rows(t, shape, dtype, name, device):
                          f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}")
     if t.device != device:
         raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
-    return t.stride(0), t.stride(1)
+    # the stride of a single token or head is never used, whatever it says
+    return t.stride(0) if shape[0] > 1 else 0, t.stride(1) if shape[1] > 1 else 0
 
 
 def store_cache(K: torch.Tensor, V: torch.Tensor, cache: dict, slots: torch.Tensor,

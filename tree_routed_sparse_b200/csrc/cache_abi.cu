@@ -11,7 +11,10 @@ namespace {
 
 constexpr int kMaxRequests = 8192;  // the plan keeps two words a request in shared memory
 constexpr int kMaxGroup = 64;
+constexpr int kMaxHeads = 65535;           // a grid's second axis
+constexpr int64_t kMaxLength = 1 << 30;    // tokens of a block table's row: sums of two stay 32 bits
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool good_block_size(int32_t b) { return b == 16 || b == 32 || b == 64 || b == 128; }
@@ -22,6 +25,7 @@ alhr_status check_cache(const alhr_cache* c) {
   if (!good_block_size(c->block_size)) return ALHR_ERR_UNSUPPORTED;
   if (c->d != 64 && c->d != 128) return ALHR_ERR_UNSUPPORTED;
   if (c->code != ALHR_CODE_INT8 && c->code != ALHR_CODE_E4M3) return ALHR_ERR_INVALID_ARG;
+  if (c->heads > kMaxHeads) return ALHR_ERR_UNSUPPORTED;
   const int64_t rows_per_head = int64_t(c->blocks) * c->block_size;
   if (rows_per_head > INT32_MAX || rows_per_head * c->heads > INT32_MAX)
     return ALHR_ERR_UNSUPPORTED;
@@ -30,7 +34,7 @@ alhr_status check_cache(const alhr_cache* c) {
 
 alhr_status check_cache_memory(const alhr_cache* c) {
   if (!c->k || !c->v || !c->k_scale || !c->v_scale) return ALHR_ERR_INVALID_ARG;
-  if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scale) || !aligned16(c->v_scale))
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(c->k_scale) || !aligned4(c->v_scale))
     return ALHR_ERR_INVALID_ARG;
   return ALHR_OK;
 }
@@ -79,7 +83,7 @@ alhr_status check_queries(const alhr_cache* c, const alhr_cache_queries* q) {
   if (!std::isfinite(log2_scale(q->scale))) return ALHR_ERR_INVALID_ARG;
   if (q->q_heads / c->heads > kMaxGroup || q->requests > kMaxRequests) return ALHR_ERR_UNSUPPORTED;
   if (int64_t(q->tokens) * q->q_heads > INT32_MAX) return ALHR_ERR_UNSUPPORTED;
-  if (int64_t(q->max_blocks) * c->block_size > INT32_MAX) return ALHR_ERR_UNSUPPORTED;
+  if (int64_t(q->max_blocks) * c->block_size > kMaxLength) return ALHR_ERR_UNSUPPORTED;
   return ALHR_OK;
 }
 
@@ -112,12 +116,15 @@ alhr_status alhr_plan_blocks(int32_t requests, int32_t max_blocks, int32_t block
     return ALHR_ERR_INVALID_ARG;
   if (!good_block_size(block_size)) return ALHR_ERR_UNSUPPORTED;
   if (requests > kMaxRequests) return ALHR_ERR_UNSUPPORTED;
-  if (int64_t(max_blocks) * block_size > INT32_MAX) return ALHR_ERR_UNSUPPORTED;
+  if (int64_t(max_blocks) * block_size > kMaxLength) return ALHR_ERR_UNSUPPORTED;
   if (!free_first || !free_next || !q_start) return ALHR_ERR_INVALID_ARG;
   if (requests > 0 && (!ctx_len || !new_len || !block_table || !seq_len))
     return ALHR_ERR_INVALID_ARG;
   if (tokens > 0 && (!slots || !positions)) return ALHR_ERR_INVALID_ARG;
   if (free_count > 0 && !free_blocks) return ALHR_ERR_INVALID_ARG;
+  // every CTA reads these while another one may have written its outputs already
+  if (free_next == free_first || (requests > 0 && (seq_len == ctx_len || seq_len == new_len)))
+    return ALHR_ERR_INVALID_ARG;
   const alhr::PlanArgs a{requests, max_blocks, block_size, blocks,  tokens,  free_count,
                          ctx_len,  new_len,    block_table, free_blocks, free_first, q_start,
                          seq_len,  slots,      positions,  free_next, dev_err};
@@ -232,7 +239,7 @@ alhr_status alhr_attend_cache_selected(const alhr_cache* cache,
   if (q.max_keys > 96 || q.q_heads / cache->heads > kMaxGroup) return ALHR_ERR_UNSUPPORTED;
   if (int64_t(q.batch) * q.q_heads > INT32_MAX ||
       int64_t(q.batch) * q.q_heads * q.nq > INT32_MAX ||
-      int64_t(q.max_blocks) * cache->block_size > INT32_MAX)
+      int64_t(q.max_blocks) * cache->block_size > kMaxLength)
     return ALHR_ERR_UNSUPPORTED;
   if (q.nq == 0) return ALHR_OK;  // nothing to read or write
   s = check_cache_memory(cache);
