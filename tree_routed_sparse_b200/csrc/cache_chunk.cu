@@ -566,18 +566,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
         }
         if (!done) {
+          // by 32 columns: most of what a mask cuts is seen by the whole warp or by none of it
           float top = -INFINITY;  // the largest x of the row
-#pragma unroll 2
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
+            const int here = seen - c * 32;
+            if (!__any_sync(0xffffffffu, here > 0)) break;
             uint32_t v[32];
             tmem_ld32(v, s_col + c * 32);
             wait_ld();
+            if (__any_sync(0xffffffffu, here < 32)) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (k >= here) v[k] = 0xff800000u;  // -infinity
+            }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              float x = -INFINITY;
+              float x = __uint_as_float(v[u * 16]);
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
-                if (c * 32 + u * 16 + k < seen) x = fmaxf(x, __uint_as_float(v[u * 16 + k]));
+              for (int k = 1; k < 16; ++k) x = fmaxf(x, __uint_as_float(v[u * 16 + k]));
               const float4 f = sc[c * 2 + u];
               // -infinity stays where the factor is 0
               top = fmaxf(top, x == -INFINITY ? x : fmaf(x, qs * f.x, f.y));
@@ -603,29 +610,39 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
           }
           const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll 2
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            uint32_t v[32], p[16];
-            tmem_ld32(v, s_col + c * 32);
-            wait_ld();
+            const int here = seen - c * 32;
+            uint32_t p[16];
+            if (!__any_sync(0xffffffffu, here > 0)) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const float4 f = sc[c * 2 + u];
-              const float f1 = qs * f.x, f0 = f.y - base;
-              float part = 0.f;
+              for (int k = 0; k < 16; ++k) p[k] = 0u;
+            } else {
+              uint32_t v[32];
+              tmem_ld32(v, s_col + c * 32);
+              wait_ld();
+              if (__any_sync(0xffffffffu, here < 32)) {
 #pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                float x0 = exp2_fast(fmaf(__uint_as_float(v[u * 16 + k]), f1, f0));
-                float x1 = exp2_fast(fmaf(__uint_as_float(v[u * 16 + k + 1]), f1, f0));
-                if (c * 32 + u * 16 + k >= seen) x0 = 0.f;
-                if (c * 32 + u * 16 + k + 1 >= seen) x1 = 0.f;
-                part += x0 + x1;
-                p[u * 8 + k / 2] = pack2(x0, x1, true);
+                for (int k = 0; k < 32; ++k)
+                  if (k >= here) v[k] = 0xff800000u;
               }
-              l = fmaf(part, f.z, l);
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const float4 f = sc[c * 2 + u];
+                // not 0: a masked score stays -infinity (the largest, 2^29, times 1e-37 is nothing)
+                const float f1 = fmaxf(qs * f.x, 1e-37f), f0 = f.y - base;
+                float part = 0.f;
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                  const float x0 = exp2_fast(fmaf(__uint_as_float(v[u * 16 + k]), f1, f0));
+                  const float x1 = exp2_fast(fmaf(__uint_as_float(v[u * 16 + k + 1]), f1, f0));
+                  part += x0 + x1;
+                  p[u * 8 + k / 2] = pack2(x0, x1, true);
+                }
+                l = fmaf(part, f.z, l);
+              }
             }
-            // over scores that have been read
-            tmem_st16(s_col + c * 16, p);
+            tmem_st16(s_col + c * 16, p);  // over scores that have been read
           }
         }
         wait_st();
