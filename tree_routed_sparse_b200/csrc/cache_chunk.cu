@@ -3,18 +3,23 @@
 // Mathematics as in cache_decode.cu: x_j = s_j log2 e + log2 v_scale_j, weights 2^(x_j - M) times
 // value codes, l = sum w_j / v_scale_j.
 //
-// What bounds it: the two products, 4 d flops a row and key, and one power of two a row and key;
-// at d = 128 the tensor core and the special-function unit need the same time. One CTA a
-// multiprocessor takes 256 query rows (two tiles of 128) of one key head and walks key tiles of
-// 128. Four warps load codes to registers, widen them to halves (exact) and write them to shared
-// memory in the core-matrix layout of tcgen05 (8 rows of 16 bytes): for the keys (rows of the
-// second operand) K-major, and the same bytes read MN-major are the values' operand, so nothing is
-// transposed. One lane of each tile of rows asks
-// for its products: S_i = Q_i K^T into tensor memory, and O_i += P_i V
-// with P_i read from tensor memory, where the rows' threads put it in place of S_i. While the
-// tensor core works on one tile of rows the threads of the other one take their powers of two.
-// Rows of a request are (token, head of the group) pairs, so that grouped heads share every key
-// tile.
+// What bounds it: the two products, 4 d flops a row and key, and one power of two a row and key; at
+// d = 128 the tensor core, the special-function unit and the operands' way through shared memory
+// need the same time (2048 cycles for 256 rows and 128 keys), at d = 64 the powers of two do. The
+// rows' chain (scores, weights, sum) is what is left over: measured 1.13 ms for 2 x 2048 rows x 32
+// heads behind 14,336 keys at d = 128 (910 TFLOP/s, 0.55 of the measured bf16 rate; the tensor
+// core works 41 % of the time, the special-function unit 43 %).
+//
+// One CTA a multiprocessor takes 256 query rows (two tiles of 128) of one key head and walks key
+// tiles of 128. Eight warps load codes to registers, widen them to halves (exact) and write them to
+// shared memory in the core-matrix layout of tcgen05 (8 rows of 16 bytes): for the keys (rows of
+// the second operand) K-major, and the same bytes read MN-major are the values' operand, so nothing
+// is transposed. The rows' warps, a thread a row, hold the rest: one lane of each tile of rows asks
+// for its products, S_i = Q_i K^T into tensor memory and O_i += P_i V with P_i read from tensor
+// memory, where the rows' threads put it in place of S_i. While the tensor core works on one tile
+// of rows the threads of the other one take their powers of two. A warp of its own for the products
+// was slower (1.14 ms): it has to be woken twice a tile. Rows of a request are (token, head of the
+// group) pairs, so that grouped heads share every key tile.
 //
 // As in cache_decode.cu the key tiles of all units form one list of which every CTA takes an
 // equal, contiguous piece; units that span pieces leave partial sums that a second kernel joins.

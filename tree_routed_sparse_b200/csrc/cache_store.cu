@@ -1,7 +1,10 @@
 // cache_store.cu -- new tokens into the paged 8-bit cache, and its numbers back.
 //
 // Both are bound by memory: a stored number is read once (2 bytes) and written once (1 byte), a
-// loaded one the other way round.
+// loaded one the other way round. Measured, keys and values of 17.9 K tokens x 8 heads, d = 128, e4m3
+// blocks of 16, stored and read back: 66 us (3.3 TB/s, half the copy rate; the first-level cache
+// is busy 80 % of the time). One appended token of 64 sequences, stored and its blocks read back:
+// 8.4 us, two launches.
 //
 // store: one warp takes one run (rows of consecutive slots of one block) of one head, keys or
 // values: the run's largest magnitude, the block's new scale, the codes of the rows before the run
