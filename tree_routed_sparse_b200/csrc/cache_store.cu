@@ -2,15 +2,14 @@
 //
 // Both are bound by memory: a stored number is read once (2 bytes) and written once (1 byte), a
 // loaded one the other way round. Measured, keys and values of 17.9 K tokens x 8 heads, d = 128, e4m3
-// blocks of 16, stored and read back: 66 us (3.3 TB/s, half the copy rate; the first-level cache
-// is busy 80 % of the time). One appended token of 64 sequences, stored and its blocks read back:
-// 8.4 us, two launches.
+// blocks of 16, stored and read back: 51 us (4.3 TB/s, 0.66 of the copy rate). One appended token of
+// 64 sequences, stored and its blocks read back: 7.2 us, two launches.
 //
 // store: one warp takes one run (rows of consecutive slots of one block) of one head, keys or
 // values: the run's largest magnitude, the block's new scale, the codes of the rows before the run
 // if the scale grew, the codes of the run. A pass covers 32 / (d / 8) rows, eight numbers a lane;
-// the first eight passes stay in registers between the maximum and the codes, the rest are read
-// again (from L2). The quotient x / s is one rounding of the exact one, by Markstein's correction
+// the first eight passes (four of fp32) stay in registers between the maximum and the codes, the
+// rest are read again (from L2). The quotient x / s is one rounding of the exact one, by Markstein's correction
 // of x * (1 / s) (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
 // processor", 1990): three operations where a division takes about ten.
 #include "cache_mma.cuh"
@@ -20,7 +19,6 @@ namespace alhr {
 namespace {
 
 constexpr int kStoreWarps = 4;
-constexpr int kKept = 8;
 
 template <int T>
 struct Raw8 {
@@ -63,17 +61,6 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8]) {
   return make_uint2(w[0], w[1]);
 }
 
-// Any numbers: infinities saturate, NaN becomes 0.
-template <int CODE>
-__device__ __noinline__ uint2 encode8_any(float (&x)[8], float s) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    x[j] = __fdiv_rn(x[j], s);
-    x[j] = x[j] != x[j] ? 0.f : fminf(fmaxf(x[j], -448.f), 448.f);
-  }
-  return encode8<CODE>(x);
-}
-
 template <int CODE>
 __device__ __forceinline__ void decode4(uint32_t w, float* x) {
   uint32_t lo, hi;
@@ -87,6 +74,7 @@ __device__ __forceinline__ void decode4(uint32_t w, float* x) {
 template <int D, int CODE, int T>
 __global__ void __launch_bounds__(kStoreWarps * 32, 6) store_kernel(const StoreArgs a, const int per) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes a row, rows a pass
+  constexpr int kKept = T == ALHR_TYPE_FP32 ? 4 : 8;  // passes kept in registers (32 of them)
   constexpr float kFull = CODE == ALHR_CODE_INT8 ? 127.f : 256.f;
   const int lane = threadIdx.x & 31;
   const int bs = a.c.bs, heads = a.c.heads;
@@ -95,8 +83,9 @@ __global__ void __launch_bounds__(kStoreWarps * 32, 6) store_kernel(const StoreA
   const int hw = blockIdx.y * kStoreWarps + (threadIdx.x >> 5);
   if (hw >= 2 * heads) return;
   const int which = hw >= heads, h = hw - which * heads;
-  const void* const x = a.x[which];
-  const long long step = a.token_stride[which];
+  const void* const x = which ? a.x[1] : a.x[0];
+  const long long step = which ? a.token_stride[1] : a.token_stride[0];
+  const long long head_at = (which ? a.head_stride[1] : a.head_stride[0]) * h;
   const int sub = lane % kLanes, row = lane / kLanes;
   const long long t0 = static_cast<long long>(blockIdx.x) * per;
   const int look = static_cast<int>(min(static_cast<long long>(per), a.tokens - t0));
@@ -134,7 +123,7 @@ __global__ void __launch_bounds__(kStoreWarps * 32, 6) store_kernel(const StoreA
       }
     }
     const int block = static_cast<int>(s0 >> a.c.bs_log);
-    const long long x0 = t * step + static_cast<long long>(h) * a.head_stride[which] + sub * 8;
+    const long long x0 = t * step + head_at + sub * 8;
 
     Raw8<T> kept[kKept];
 #pragma unroll
@@ -189,18 +178,17 @@ __global__ void __launch_bounds__(kStoreWarps * 32, 6) store_kernel(const StoreA
     auto put = [&](const Raw8<T>& r, int i) {
       float v[8];
       r.numbers(v);
-      uint2 c;
-      if (odd) {
-        c = encode8_any<CODE>(v, s);
-      } else {
+      if (odd) {  // NaN becomes 0, an infinity what saturates; finite numbers are below 256 s
+        const float most = fminf(s * 512.f, 3e38f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float q = __fmul_rn(v[j], inv);
-          v[j] = __fmaf_rn(__fmaf_rn(-q, s, v[j]), inv, q);
-        }
-        c = encode8<CODE>(v);
+        for (int j = 0; j < 8; ++j) v[j] = v[j] == v[j] ? fminf(fmaxf(v[j], -most), most) : 0.f;
       }
-      *reinterpret_cast<uint2*>(codes + static_cast<long long>(off + i) * D) = c;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float q = __fmul_rn(v[j], inv);
+        v[j] = __fmaf_rn(__fmaf_rn(-q, s, v[j]), inv, q);
+      }
+      *reinterpret_cast<uint2*>(codes + static_cast<long long>(off + i) * D) = encode8<CODE>(v);
     };
 #pragma unroll
     for (int p = 0; p < kKept; ++p)
@@ -238,6 +226,7 @@ __global__ void __launch_bounds__(256) load_kernel(const LoadArgs a) {
   for (int p = threadIdx.x; p < all; p += blockDim.x) {
     const int sub = p % kPieces, hw = p / kPieces;
     const int which = hw >= heads, h = hw - which * heads;
+    void* const to = which ? a.x[1] : a.x[0];
     const uint8_t* const codes = (which ? a.c.v : a.c.k) + sub * 8;
     const float* const scales = (which ? a.c.v_scale : a.c.k_scale) + h;
     uint2 c[kTokens];
@@ -263,12 +252,12 @@ __global__ void __launch_bounds__(256) load_kernel(const LoadArgs a) {
       for (int j = 0; j < 8; ++j) v[j] = slot[i] >= 0 ? __fmul_rn(v[j], s[i]) : 0.f;
       const long long at = ((t0 + i) * heads + h) * D + sub * 8;
       if constexpr (T == ALHR_TYPE_FP32) {
-        float4* q = reinterpret_cast<float4*>(static_cast<float*>(a.x[which]) + at);
+        float4* q = reinterpret_cast<float4*>(static_cast<float*>(to) + at);
         q[0] = make_float4(v[0], v[1], v[2], v[3]);
         q[1] = make_float4(v[4], v[5], v[6], v[7]);
       } else {
         constexpr bool kHalf = T == ALHR_TYPE_FP16;
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.x[which]) + at) =
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(to) + at) =
             make_uint4(pack2(v[0], v[1], kHalf), pack2(v[2], v[3], kHalf), pack2(v[4], v[5], kHalf),
                        pack2(v[6], v[7], kHalf));
       }
