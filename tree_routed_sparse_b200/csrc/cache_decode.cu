@@ -38,12 +38,10 @@ struct Tile {
   static_assert(kScaleBytes <= 64, "scales behind the codes");
 };
 
-// Key of the tile's 16-key group that row m (0..7, and m + 8 likewise) of the product stands for.
-// At d = 64 two rows share 128 bytes; this order keeps both reads below free of bank conflicts.
-template <int D>
-__device__ __forceinline__ int key_of(int m) {
-  return D == 128 ? m : (m & 4) | ((0x2130 >> (4 * (m & 3))) & 3);  // 0 3 1 2 4 7 5 6
-}
+// Key of the tile's 16-key group that row m (0..7) of the scores stands for; row m + 8 stands for the
+// key two behind it. The transposed read of the values gives a lane four consecutive keys, the
+// product wants them as two pairs eight apart: the scores' rows are in that order from the start.
+__device__ __forceinline__ int key_of(int m) { return 4 * (m >> 1) + (m & 1); }
 
 // 16-byte piece c of row `row`, where it lies in shared memory.
 template <int D>
@@ -300,33 +298,31 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
         const float sum_l = group_add(l[n][c]);
         const int col = n * 8 + 2 * t + c, row = row0 + col;
         if (row >= cur.q.rows) continue;
-        float y[D / 8];  // numbers [g * D / 8, (g + 1) * D / 8) of the row
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          y[2 * s] = o[n][s][c];
-          y[2 * s + 1] = o[n][s][2 + c];
-        }
+        // numbers 16 k + g and 16 k + 8 + g of the row
         if (from_start && to_end) {
           const float inv = sum_l > 0.f ? 1.f / sum_l : 0.f;
           const int tok = row / a.group;
           const long long at = static_cast<long long>(cur.q.q_lo + tok) * a.q_heads +
                                cur.h * a.group + (row - tok * a.group);
-          uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D + g * (D / 8));
+          uint16_t* const p = static_cast<uint16_t*>(a.out) + at * D + g;
 #pragma unroll
-          for (int i = 0; i < D / 64; ++i)
-            p[i] = make_uint4(pack2(y[8 * i] * inv, y[8 * i + 1] * inv, a.fp16),
-                              pack2(y[8 * i + 2] * inv, y[8 * i + 3] * inv, a.fp16),
-                              pack2(y[8 * i + 4] * inv, y[8 * i + 5] * inv, a.fp16),
-                              pack2(y[8 * i + 6] * inv, y[8 * i + 7] * inv, a.fp16));
+          for (int k = 0; k < KS; ++k) {
+            const uint32_t w = pack2(o[n][k][c] * inv, o[n][k][2 + c] * inv, a.fp16);
+            p[16 * k] = static_cast<uint16_t>(w);
+            p[16 * k + 8] = static_cast<uint16_t>(w >> 16);
+          }
           if (a.lse && g == 0)
             a.lse[at] = sum_l > 0.f ? (m[n][c] + log2f(sum_l)) * 0.6931471805599453f : -INFINITY;
         } else {
-          float* part = space.part + (static_cast<long long>(piece) * 2 + (from_start ? 1 : 0)) *
-                                         (ROWS * (D + 2));
-          float4* p = reinterpret_cast<float4*>(part + col * D + g * (D / 8));
+          float* const part = space.part +
+                              (static_cast<long long>(piece) * 2 + (from_start ? 1 : 0)) *
+                                  (ROWS * (D + 2));
+          float* const p = part + col * D + g;
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i)
-            p[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          for (int k = 0; k < KS; ++k) {
+            p[16 * k] = o[n][k][c];
+            p[16 * k + 8] = o[n][k][2 + c];
+          }
           if (g == 0) {
             part[ROWS * D + col] = m[n][c];
             part[ROWS * D + ROWS + col] = sum_l;
@@ -360,12 +356,12 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[u][n][i] = 0.f;
-      const int r0 = u * 16 + key_of<D>(g);
-      uint32_t w0[D / 16], w1[D / 16];  // D / 4 codes of rows g and g + 8
+      const int r0 = u * 16 + key_of(g);
+      uint32_t w0[D / 16], w1[D / 16];  // D / 4 codes of two keys
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
         const uint4 x = lds128(base + piece_offset<D>(r0, t * (D / 64) + i));
-        const uint4 y = lds128(base + piece_offset<D>(r0 + 8, t * (D / 64) + i));
+        const uint4 y = lds128(base + piece_offset<D>(r0 + 2, t * (D / 64) + i));
         w0[4 * i] = x.x; w0[4 * i + 1] = x.y; w0[4 * i + 2] = x.z; w0[4 * i + 3] = x.w;
         w1[4 * i] = y.x; w1[4 * i + 1] = y.y; w1[4 * i + 2] = y.z; w1[4 * i + 3] = y.w;
       }
@@ -380,7 +376,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
       const uint4 sc = lds128(base + kStageBytes + u * 16);
       const float vs = fmaxf(__uint_as_float(sc.y), kTinyScale);
       add[u] = sc.z ? __log2f(vs) : -INFINITY;
-      inv_vs[u] = sc.z ? __frcp_rn(vs) : 0.f;
+      inv_vs[u] = sc.z ? rcp_fast(vs) : 0.f;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -394,12 +390,12 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
     if (key0 + Tile<D>::kKeys > see_min) {  // some row does not see the whole tile
 #pragma unroll
       for (int u = 0; u < SUBS; ++u) {
-        const int k0 = key0 + u * 16 + key_of<D>(g);
+        const int k0 = key0 + u * 16 + key_of(g);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (k0 + (i >> 1) * 8 >= see[n][i & 1]) s[u][n][i] = -INFINITY;
+            if (k0 + (i >> 1) * 2 >= see[n][i & 1]) s[u][n][i] = -INFINITY;
       }
     }
     // M moves only when it has to: the largest weight is between 2^7 and 2^15
@@ -448,34 +444,23 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
         pf[u][n][1] = transpose8x8(pack2(p2, p3, true));
       }
     }
-    // values: lane (g, t) takes numbers [g D / 8, (g + 1) D / 8) of four keys
+    // values: the transposed read gives lane (g, t) keys 4 t .. 4 t + 3 of numbers g and g + 8 of two
+    // 16-byte pieces
 #pragma unroll
     for (int u = 0; u < SUBS; ++u) {
-      constexpr int W = D / 32;  // words of a row
-      uint32_t v[4][W];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = u * 16 + key_of<D>(2 * t + (i & 1)) + (i >> 1) * 8;
-        if constexpr (D == 128) {
-          const uint4 x = lds128(base + kStageBytes / 2 + piece_offset<D>(row, g));
-          v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
-        } else {
-          const uint2 x = lds64(base + kStageBytes / 2 + piece_offset<D>(row, g >> 1) + (g & 1) * 8);
-          v[i][0] = x.x; v[i][1] = x.y;
-        }
-      }
+      for (int i = 0; i < KS / 2; ++i) {
+        uint32_t v[4];
+        read_transposed(v, base + kStageBytes / 2 +
+                               piece_offset<D>(u * 16 + (lane & 15), 2 * i + (lane >> 4)));
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        // pairs of keys of the same number: {a, b} of numbers 4 w .. 4 w + 3
-        uint32_t x0, x1, x2, x3, y0, y1, y2, y3;
-        widen4<CODE>(prmt(v[0][w], v[1][w], 0x5140), x0, x1);
-        widen4<CODE>(prmt(v[0][w], v[1][w], 0x7362), x2, x3);
-        widen4<CODE>(prmt(v[2][w], v[3][w], 0x5140), y0, y1);
-        widen4<CODE>(prmt(v[2][w], v[3][w], 0x7362), y2, y3);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t a0, a1, a2, a3;
+          widen4<CODE>(v[2 * h], a0, a2);
+          widen4<CODE>(v[2 * h + 1], a1, a3);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma16816(o[n][2 * w], x0, x1, y0, y1, pf[u][n][0], pf[u][n][1]);
-          mma16816(o[n][2 * w + 1], x2, x3, y2, y3, pf[u][n][0], pf[u][n][1]);
+          for (int n = 0; n < NT; ++n)
+            mma16816(o[n][2 * i + h], a0, a1, a2, a3, pf[u][n][0], pf[u][n][1]);
         }
       }
     }
