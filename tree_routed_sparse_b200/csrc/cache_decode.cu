@@ -8,13 +8,14 @@
 // rounded at 2^-11 of themselves. l is summed from the fp32 weights.
 //
 // What bounds it: the codes have to be read once, 2 d bytes a key and head; everything else is
-// there to keep the memory busy (4 sequences x 8 heads x 262,144 e4m3 keys, d = 128: 312 us, 6.9
-// TB/s; 64 sequences of up to 16,384 int8 keys, 32 query heads over 8: 203 us, 5.8 TB/s, where the
-// int8 codes' widening takes the issue slots). The tiles of all (request, key head, row group)
+// there to keep the memory busy (64 sequences of up to 16,384 int8 keys, 32 query heads over 8, d =
+// 128: 190 us, 6.2 TB/s; 4 sequences x 8 heads x 262,144 e4m3 keys: 341 us, 6.3 TB/s; 0.94 and 0.96
+// of the copy rate). The tiles of all (request, key head, row group)
 // units form one list, and each warp of the GPU takes an equal, contiguous piece of it: no unit is
 // too short or too long, and no warp waits for another one. A warp copies its tiles (32 keys at d =
 // 128, 64 at d = 64: 8 KB) kStages ahead into its own piece of shared memory, 192 KB of copies in
-// flight a multiprocessor, converts the codes to halves in registers and uses the warp-wide matrix
+// flight a multiprocessor, reads the values transposed (203 -> 190 us against interleaving bytes of
+// key pairs in registers), converts the codes to halves in registers and uses the warp-wide matrix
 // product, which costs the same for one query row as for eight. A unit inside one warp's piece is written at
 // once; one that spans pieces leaves partial sums (O, M, l), which a second kernel joins in the
 // order of the pieces.
