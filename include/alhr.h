@@ -59,9 +59,10 @@
  *   ALHR_DEVERR_INDEX        alhr_attend: an idx entry outside [0, i] is skipped (weight 0);
  *   ALHR_DEVERR_TIMEOUT      alhr_topk_labels: a bounded wait on the tensor core ran out; the
  *                            rows of that CTA's query tile (128 queries) are NOT written, so
- *                            labels and scores there keep whatever the buffers held before.
- * Kernels contain no unbounded loop; the only waits (alhr_topk_labels, on its own MMAs) are
- * bounded.
+ *                            labels and scores there keep whatever the buffers held before
+ *                            (alhr_attend_cache sets it too, see alhr_cache.h).
+ * Kernels contain no unbounded loop; the only waits (alhr_topk_labels and alhr_attend_cache of
+ * alhr_cache.h, on their own MMAs and between the warps that feed them) are bounded.
  */
 #ifndef ALHR_H
 #define ALHR_H

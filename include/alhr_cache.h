@@ -166,7 +166,10 @@ ALHR_API size_t alhr_attend_cache_workspace(const alhr_cache* cache,
  *   lse       device float [tokens][q_heads], or NULL
  *   workspace device, 16-byte aligned; used from launch to completion of this call, so calls that
  *             may run at the same time need one each
- * The sums are fp32; the result of a call depends on its inputs and the device alone.
+ * The sums are fp32; the result of a call depends on its inputs and the device alone. Requests
+ * with more than 16 rows per key/value head are computed on the tensor core, whose waits are
+ * bounded: should one run out (not expected), ALHR_DEVERR_TIMEOUT is set and out and lse of the
+ * call are not to be used.
  */
 ALHR_API alhr_status alhr_attend_cache(const alhr_cache* cache, const alhr_cache_queries* queries,
                                        const void* Q, const int32_t* block_table,

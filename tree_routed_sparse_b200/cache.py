@@ -223,7 +223,8 @@ def attend_cache(Q: torch.Tensor, cache: dict, block_table: torch.Tensor, ctx_le
     chooses the kernels; unknown: None); scale: 1 / sqrt(d) unless given. Returns out, of Q's type
     (rows outside every request keep what they hold), and lse float32 [tokens, q_heads] if asked
     for. workspace: uint8, at least attend_cache_workspace(...) bytes; calls that may run at the
-    same time need one each."""
+    same time need one each. dev_err: DEVERR_BLOCK for a block number outside the cache;
+    DEVERR_TIMEOUT, not expected, where the outputs are not to be used."""
     dev = _cuda(Q, "Q")
     c = _struct(cache, dev)
     if Q.dim() != 3 or Q.dtype not in (torch.bfloat16, torch.float16):
