@@ -198,6 +198,31 @@ def test_store_special_values(C, dtype):
     assert err.item() == 0
 
 
+@pytest.mark.parametrize("dtype", [I8, E4])
+@pytest.mark.parametrize("src", [torch.bfloat16, torch.float32])
+def test_store_infinities_beside_the_largest_numbers(C, dtype, src):
+    """Infinities and NaN in runs whose finite numbers reach the top of the type: the finite ones
+    are stored as without them, the infinities saturated whatever the scale."""
+    top = torch.finfo(src).max
+    x = torch.linspace(-1, 1, 64).repeat(3, 1, 1)
+    x[0] *= top
+    x[0, 0, :3] = torch.tensor([math.inf, -math.inf, math.nan])
+    x[1, 0, 5] = -top
+    x[1, 0, 6] = math.inf
+    x[2, 0, 7] = -math.inf  # the largest finite number of this run is 1
+    x = x.to(src)
+    slots = torch.tensor([0, 1, 16])
+    cache = C.alloc_cache(2, 1, 16, 64, dtype)
+    codes, scale = torch.zeros(2, 1, 16, 64).to(dtype), torch.zeros(2, 1)
+    store_ref(x.float(), codes, scale, slots)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    C.store_cache(x.cuda(), x.cuda(), cache, slots.cuda(), dev_err=err)
+    assert err.item() == C.DEVERR_NONFINITE
+    for key in ("k", "v"):
+        assert torch.equal(bits(cache[key].cpu()), bits(codes))
+        assert torch.equal(cache[key + "_scale"].cpu(), scale)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
 @pytest.mark.parametrize("code", [I8, E4])
 @pytest.mark.parametrize("d,bs", [(64, 128), (128, 16)])
