@@ -157,10 +157,11 @@ ALHR_API size_t alhr_attend_cache_workspace(const alhr_cache* cache,
  * Rows [q_start[r], q_start[r + 1]) of Q belong to request r; row q_start[r] + t stands at
  * position ctx_len[r] + t and sees the keys [0, min(ctx_len[r] + t + 1, seq_len[r])):
  *   s_j = scale * (q . k_j),  out = sum_j exp(s_j) v_j / sum_j exp(s_j),  lse = ln sum_j exp(s_j)
- * A row that sees no key gets zeros and lse = -infinity. Rows outside every request keep what
- * they hold. seq_len is cut at max_blocks * block_size, q_start at [0, tokens]; keys in blocks
- * outside [0, blocks) are left out and set ALHR_DEVERR_BLOCK. Only table entries, scales and
- * blocks that hold visible keys are read, and codes behind seq_len have no effect.
+ * A row that sees no key gets zeros and lse = -infinity. A NaN in another row of Q makes the
+ * row's out and lse NaN and touches no other row. Rows outside every request keep what they hold.
+ * seq_len is cut at max_blocks * block_size, q_start at [0, tokens]; keys in blocks outside
+ * [0, blocks) are left out and set ALHR_DEVERR_BLOCK. Only table entries, scales and blocks that
+ * hold visible keys are read, and codes behind seq_len have no effect.
  *   Q         device, type as given; base 16-byte aligned
  *   out       device [tokens][q_heads][d], type of Q, 16-byte aligned
  *   lse       device float [tokens][q_heads], or NULL
@@ -195,7 +196,8 @@ typedef struct {
  * Row t stands at position ctx_len[b] + t; entries of idx outside
  * [0, min(ctx_len[b] + t + 1, seq_len[b], max_blocks * block_size)) are skipped and set
  * ALHR_DEVERR_INDEX, entries in blocks outside [0, blocks) are skipped and set
- * ALHR_DEVERR_BLOCK. A position that is named twice counts twice. A row without keys gets zeros.
+ * ALHR_DEVERR_BLOCK. A position that is named twice counts twice. A row without keys gets zeros,
+ * one with a NaN in Q gets NaN.
  *   Q            device, type as given, [batch][q_heads][nq][d], 16-byte aligned
  *   block_table  device int32 [batch][max_blocks]
  *   idx, count   device int32 [batch][q_heads][nq][max_keys], [batch][q_heads][nq]

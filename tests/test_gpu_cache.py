@@ -442,6 +442,30 @@ def test_attend_queries_large_and_small(C, qt, new):
     check(C, s)
 
 
+@pytest.mark.parametrize("ctx,new", [
+    ([3, 40], [1, 1]), ([20000, 40], [1, 1]), ([3, 40], [3, 2]),
+    ([0, 100], [70, 40]), ([9000, 100], [70, 40])])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_attend_nan_stays_in_its_row(C, ctx, new, bad):
+    """A NaN in a query gives NaN in that row's output (an infinity too: inf - inf in the softmax,
+    and inf * 0), and touches no other row: whole units and those that are joined."""
+    s = make(ctx, new, 8, 2, 64, 16, I8, torch.bfloat16)
+    c = s["cache"]
+    c["k"][..., 0] = 5  # a number that no product with an infinity loses
+    run = lambda: C.attend_cache(s["q"], c, s["table"], s["ctx"], s["seq"], s["start"],
+                                 max_q=s["max_q"], want_lse=True)
+    want = run()
+    row, head = s["q"].shape[0] // 2, 5
+    s["q"][row, head, 0] = bad
+    s["q"][0, 2, 0] = bad
+    got = run()
+    hit = torch.zeros(s["q"].shape[:2], dtype=torch.bool, device="cuda")
+    hit[row, head] = hit[0, 2] = True
+    assert bool(got["out"][hit].isnan().all()) and bool(got["lse"][hit].isnan().all())
+    for key in ("out", "lse"):
+        assert torch.equal(got[key][~hit], want[key][~hit])
+
+
 def test_attend_codes_past_32_bits(C):
     """Blocks whose bytes lie behind 2^32."""
     d, bs, hkv = 128, 128, 8
@@ -584,6 +608,23 @@ def test_selected_blocks_outside(C):
     b = C.attend_cache_selected(q, cache, table, ints([63]), ints([64]), ints([[[[0, 50]]]]),
                                 ints([[[2]]]))
     assert float((a - b).abs().max()) <= 2.0 ** -20 * float(b.abs().max())
+
+
+@pytest.mark.parametrize("qt", [torch.bfloat16, torch.float16])
+def test_selected_nan_stays_in_its_row(C, qt):
+    g = torch.Generator(device="cuda").manual_seed(4)
+    cache = random_cache(5, 2, 16, 64, I8, g, "cuda")
+    table = scattered_table([80], 16, 5, 5, g, "cuda")
+    q = torch.randn(1, 4, 3, 64, generator=g, device="cuda").to(qt)
+    idx = torch.randint(0, 70, (1, 4, 3, 40), generator=g, device="cuda").int()
+    count = torch.full((1, 4, 3), 40, dtype=torch.int32, device="cuda")
+    run = lambda: C.attend_cache_selected(q, cache, table, ints([77]), ints([80]), idx, count)
+    want = run()
+    q[0, 1, 2, 7] = math.nan
+    got = run()
+    assert bool(got[0, 1, 2].isnan().all())
+    got[0, 1, 2] = want[0, 1, 2]
+    assert torch.equal(got, want)
 
 
 # ------------------------------------------------------------------ the set together

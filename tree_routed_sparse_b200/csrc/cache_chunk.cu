@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const int tok = was_row / a.group;
           const long long at = static_cast<long long>(was.q.q_lo + tok) * a.q_heads +
                                was.h * a.group + (was_row - tok * a.group);
-          const float inv = was_l > 0.f ? 1.f / was_l : 0.f;
+          const float inv = was_l == 0.f ? 0.f : 1.f / was_l;  // no key; NaN stays
           float* part = space.part + (static_cast<long long>(piece) * 2 + (started ? 1 : 0)) *
                                          (kRows * (D + 2));
           const int pr = i * 128 + rt;
@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
           if (on && whole) {
             if (a.lse)
-              a.lse[at] = was_l > 0.f ? (was_m + log2f(was_l)) * 0.6931471805599453f : -INFINITY;
+              a.lse[at] = was_l == 0.f ? -INFINITY : (was_m + log2f(was_l)) * 0.6931471805599453f;
           } else if (on) {
             part[kRows * D + pr] = was_m;
             part[kRows * D + kRows + pr] = was_l;

@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
         if (row >= cur.q.rows) continue;
         // numbers 16 k + g and 16 k + 8 + g of the row
         if (from_start && to_end) {
-          const float inv = sum_l > 0.f ? 1.f / sum_l : 0.f;
+          const float inv = sum_l == 0.f ? 0.f : 1.f / sum_l;  // no key; NaN stays
           const int tok = row / a.group;
           const long long at = static_cast<long long>(cur.q.q_lo + tok) * a.q_heads +
                                cur.h * a.group + (row - tok * a.group);
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
             p[16 * k + 8] = static_cast<uint16_t>(w >> 16);
           }
           if (a.lse && g == 0)
-            a.lse[at] = sum_l > 0.f ? (m[n][c] + log2f(sum_l)) * 0.6931471805599453f : -INFINITY;
+            a.lse[at] = sum_l == 0.f ? -INFINITY : (m[n][c] + log2f(sum_l)) * 0.6931471805599453f;
         } else {
           float* const part = space.part +
                               (static_cast<long long>(piece) * 2 + (from_start ? 1 : 0)) *

@@ -226,14 +226,14 @@ __global__ void __launch_bounds__(kSelWarps * 32, D == 64 ? 8 : 6) selected_kern
       }
     }
     // ---- numbers g D / 8 .. + D / 8 - 1 of the output, every t has them: t writes its share
-    const float inv = l > 0.f ? wdown / l : 0.f;
+    const float inv = wdown / l;
     float* out = a.out + u * D + g * (D / 8);
 #pragma unroll
     for (int k = 0; k < KS / 2; ++k) {
       float4 y = make_float4((o[2 * k][0] + o[2 * k][1]) * inv, (o[2 * k][2] + o[2 * k][3]) * inv,
                              (o[2 * k + 1][0] + o[2 * k + 1][1]) * inv,
                              (o[2 * k + 1][2] + o[2 * k + 1][3]) * inv);
-      if (!(l > 0.f)) y = make_float4(0.f, 0.f, 0.f, 0.f);  // no key
+      if (l == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);  // no key; NaN stays
       if (t == k) reinterpret_cast<float4*>(out)[k] = y;
     }
     __syncwarp();  // every lane has read the keys

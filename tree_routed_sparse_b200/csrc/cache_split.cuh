@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendArgs 
       }
     }
     if (sub == 0) {
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // no key; NaN stays
       const int rr = p.row0 + row, tok = rr / a.group;
       const int q_lo = min(max(__ldg(a.q_start + p.r), 0), a.tokens);
       const long long at = static_cast<long long>(q_lo + tok) * a.q_heads + p.h * a.group +
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendArgs 
         *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at * D + lane * E + e) =
             pack2(acc[e] * inv, acc[e + 1] * inv, a.fp16);
       if (a.lse && lane == 0)
-        a.lse[at] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
   }
 }
