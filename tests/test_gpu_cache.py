@@ -627,6 +627,24 @@ def test_selected_nan_stays_in_its_row(C, qt):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("first", [31, 32, 64, 95])
+def test_selected_pages_of_others_have_no_effect(C, first):
+    """Entries that are skipped, more than a warp's worth of them before the first that is not, and
+    NaN in every code of the pages that are not the request's (the first page among them)."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    cache = random_cache(6, 1, 16, 128, E4, g, "cuda")
+    q = torch.randn(1, 1, 1, 128, generator=g, device="cuda").bfloat16()
+    idx = torch.full((1, 1, 1, 96), -1, dtype=torch.int32, device="cuda")
+    idx[0, 0, 0, first:] = torch.randint(0, 40, (96 - first,), generator=g, device="cuda").int()
+    want = C.attend_cache_selected(q, cache, ints([[3, 5, 2]]), ints([47]), ints([48]), idx,
+                                   ints([[[96]]]))
+    for key in ("k", "v"):
+        bits(cache[key])[[0, 1, 4]] = 0x7f
+    got = C.attend_cache_selected(q, cache, ints([[3, 5, 2]]), ints([47]), ints([48]), idx,
+                                  ints([[[96]]]))
+    assert bool(want.isfinite().all()) and torch.equal(got, want)
+
+
 # ------------------------------------------------------------------ the set together
 
 @pytest.mark.parametrize("code", [I8, E4])

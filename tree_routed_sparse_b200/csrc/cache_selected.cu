@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kSelWarps * 32, D == 64 ? 8 : 6) selected_kern
     const long long see = min(min(pos + 1, static_cast<long long>(__ldg(a.seq_len + b))), cap);
     // ---- where the keys lie
     uint32_t flags = 0;
-    int spare = 0;
+    int spare = -1, behind = 0;  // behind: groups of 32 entries before the first that has a key
 #pragma unroll
     for (int i = 0; i < kSelKeys / 32; ++i) {
       const int e = i * 32 + lane;
@@ -77,9 +77,12 @@ __global__ void __launch_bounds__(kSelWarps * 32, D == 64 ? 8 : 6) selected_kern
       // a skipped key reads the row of one that is not (in bounds, and as finite as the rest)
       const unsigned some = __ballot_sync(0xffffffffu, k.on);
       if (some) spare = __shfl_sync(0xffffffffu, k.row, __ffs(some) - 1);
-      if (!k.on) k.row = spare;
+      if (spare < 0) behind = i + 1;
+      if (!k.on) k.row = max(spare, 0);
       mine[e] = k;
     }
+    if (spare >= 0)
+      for (int i = 0; i < behind; ++i) mine[i * 32 + lane].row = spare;
     flags = __reduce_or_sync(0xffffffffu, flags);
     if (flags && lane == 0) cache_flag(a.dev_err, flags);
     // ---- the query: lane t holds numbers 16 (4 j + t) .. + 15, scaled by a power of two
