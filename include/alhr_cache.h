@@ -15,8 +15,10 @@
  * Cache layout (row-major, contiguous, device memory; codes 16-byte, scales 4-byte aligned):
  *   k, v             8-bit codes [blocks][heads][block_size][d]
  *   k_scale, v_scale float       [blocks][heads]
- *   A key or value is code * scale of its block and head; scales are not negative. Codes are int8 in [-127, 127] or e4m3
- *   (4 exponent bits, 3 mantissa bits, no infinities).
+ *   A key or value is code * scale of its block and head; scales are finite and not negative.
+ *   Codes are int8 in [-127, 127] or e4m3 (4 exponent bits, 3 mantissa bits, no infinities) that
+ *   is not NaN, as alhr_store_cache writes them. A NaN in what some row of a request sees may
+ *   reach the request's other rows too.
  * A slot is block * block_size + offset (64 bits). Position p of request r lies in block
  * block_table[r][p / block_size] at offset p % block_size.
  *
