@@ -207,10 +207,72 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendArgs 
   }
 }
 
+// The same for units of many rows, of which most span two or three pieces: a thread takes four
+// numbers of two rows through all partials, with a running M, so that a row costs two dependent
+// trips to memory (the unit, its partials) and all rows of a CTA make them together: 9 us for 144
+// units of 256 rows in 31 tiles a piece, d = 64, where a warp for each pair of rows took 20 and two
+// passes over the partials 12.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(256) join_rows_kernel(const AttendArgs a, const JoinSpace space) {
+  wait_for_previous();
+  constexpr int kLanes = D / 4, kAtOnce = 256 / kLanes, kEach = 2, kHere = kEach * kAtOnce;
+  constexpr long long kStep = ROWS * (D + 2);
+  const int piece = blockIdx.x, row0 = blockIdx.y * kHere + threadIdx.x / kLanes;
+  const JoinMeta p = space.meta[piece];
+  if (p.last < 0 || static_cast<int>(blockIdx.y) * kHere >= p.rows) return;
+  const int n = p.last - piece + 1, col = threadIdx.x % kLanes * 4;
+  // partials: slot 1 of this piece, slot 0 of the pieces behind it
+  const float* const slots = space.part + piece * 2 * kStep;
+  auto part = [&](int i) { return slots + (i == 0 ? kStep : 2 * i * kStep); };
+  float m[kEach], l[kEach], acc[kEach][4];
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    m[k] = -INFINITY;
+    l[k] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[k][e] = 0.f;
+  }
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float* const x = part(i);
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int row = row0 + k * kAtOnce;
+      const float4 y = *reinterpret_cast<const float4*>(x + row * D + col);
+      const float mi = x[ROWS * D + row], li = x[ROWS * D + ROWS + row];
+      const float mn = fmaxf(m[k], mi), base = mn == -INFINITY ? 0.f : mn;
+      const float keep = exp2_fast(m[k] - base), w = exp2_fast(mi - base);
+      m[k] = mn;
+      l[k] = fmaf(li, w, l[k] * keep);
+      acc[k][0] = fmaf(y.x, w, acc[k][0] * keep);
+      acc[k][1] = fmaf(y.y, w, acc[k][1] * keep);
+      acc[k][2] = fmaf(y.z, w, acc[k][2] * keep);
+      acc[k][3] = fmaf(y.w, w, acc[k][3] * keep);
+    }
+  }
+  const int q_lo = min(max(__ldg(a.q_start + p.r), 0), a.tokens);
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int row = row0 + k * kAtOnce;
+    if (row >= p.rows) continue;
+    const float inv = l[k] == 0.f ? 0.f : 1.f / l[k];  // no key; NaN stays
+    const int rr = p.row0 + row, tok = rr / a.group;
+    const long long at = static_cast<long long>(q_lo + tok) * a.q_heads + p.h * a.group +
+                         (rr - tok * a.group);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + col) =
+        make_uint2(pack2(acc[k][0] * inv, acc[k][1] * inv, a.fp16),
+                   pack2(acc[k][2] * inv, acc[k][3] * inv, a.fp16));
+    if (a.lse && col == 0)
+      a.lse[at] = l[k] == 0.f ? -INFINITY : (m[k] + log2f(l[k])) * 0.6931471805599453f;
+  }
+}
+
 template <int D, int ROWS>
 cudaError_t launch_join(const AttendArgs& a, const JoinSpace& space, int pieces, cudaStream_t st) {
-  return launch_behind(join_kernel<D, ROWS>, dim3(pieces, (ROWS + 15) / 16), kJoinWarps * 32, 0, st,
-                       a, space);
+  if constexpr (ROWS > 16)
+    return launch_behind(join_rows_kernel<D, ROWS>, dim3(pieces, ROWS / (512 / (D / 4))), 256, 0, st, a, space);
+  else
+    return launch_behind(join_kernel<D, ROWS>, dim3(pieces), kJoinWarps * 32, 0, st, a, space);
 }
 
 }  // namespace alhr
