@@ -117,20 +117,19 @@ cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t s
 
 constexpr int kJoinWarps = 8;
 
-// Joins the partial sums of the units that span pieces, one CTA (of ROWS / 16 along y) for each
-// piece in which such a unit begins. Up to eight warps share a row: each joins every k-th partial
-// (the lanes take 32 weights 2^(M_i - max M) at a time, so that the loads of the sums do not wait
-// for one another), then their sums are added in the order of the warps.
-template <int D, int ROWS>
+// Joins the partial sums of the units that span pieces, one CTA for each piece in which such a unit
+// begins. Up to eight warps share a row: each joins every k-th partial (the lanes take 32 weights
+// 2^(M_i - max M) at a time, so that the loads of the sums do not wait for one another), then their
+// sums are added in the order of the warps.
+template <int D, int ROWS>  // ROWS <= 16
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendArgs a,
                                                                const JoinSpace space) {
   wait_for_previous();
   constexpr int E = D / 32, kStep = ROWS * (D + 2);
   const int piece = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const JoinMeta p = space.meta[piece];
-  const int row0 = blockIdx.y * 16;
-  const int rows = min(p.rows - row0, 16);
-  if (p.last < 0 || rows <= 0) return;
+  const int rows = p.rows;
+  if (p.last < 0) return;
   int shared_by = 1;  // warps of a row
   while (rows * shared_by * 2 <= kJoinWarps) shared_by *= 2;
   __shared__ float sums[kJoinWarps][D + 2];
@@ -140,9 +139,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendArgs 
     return space.part + (static_cast<long long>(piece + i) * 2 + (i == 0 ? 1 : 0)) * kStep;
   };
   for (int r = warp / shared_by; r < rows; r += kJoinWarps / shared_by) {
-    const int row = row0 + r;
     float m = -INFINITY;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, part(i)[ROWS * D + row]);
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, part(i)[ROWS * D + r]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float base = m == -INFINITY ? 0.f : m;
@@ -153,7 +151,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendArgs 
     for (int i0 = 0; i0 < mine; i0 += 32) {
       float f = 0.f;
       if (i0 + lane < mine) {
-        const float* x = part(sub + (i0 + lane) * shared_by) + ROWS * D + row;
+        const float* x = part(sub + (i0 + lane) * shared_by) + ROWS * D + r;
         f = exp2_fast(x[0] - base);
         l = fmaf(x[ROWS], f, l);
       }
@@ -161,7 +159,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendArgs 
 #pragma unroll 8
       for (int i = 0; i < some; ++i) {
         const float w = __shfl_sync(0xffffffffu, f, i);
-        const float* x = part(sub + (i0 + i) * shared_by) + row * D + lane * E;
+        const float* x = part(sub + (i0 + i) * shared_by) + r * D + lane * E;
         if constexpr (E == 4) {
           const float4 y = *reinterpret_cast<const float4*>(x);
           acc[0] = fmaf(y.x, w, acc[0]);
@@ -193,7 +191,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendArgs 
     }
     if (sub == 0) {
       const float inv = l == 0.f ? 0.f : 1.f / l;  // no key; NaN stays
-      const int rr = p.row0 + row, tok = rr / a.group;
+      const int rr = p.row0 + r, tok = rr / a.group;
       const int q_lo = min(max(__ldg(a.q_start + p.r), 0), a.tokens);
       const long long at = static_cast<long long>(q_lo + tok) * a.q_heads + p.h * a.group +
                            (rr - tok * a.group);
@@ -211,7 +209,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendArgs 
 // numbers of two rows through all partials, with a running M, so that a row costs two dependent
 // trips to memory (the unit, its partials) and all rows of a CTA make them together: 9 us for 144
 // units of 256 rows in 31 tiles a piece, d = 64, where a warp for each pair of rows took 20 and two
-// passes over the partials 12.
+// passes over the partials 12. (O with the rows innermost would be written in whole lines, 1 us less
+// in a chunk's CTAs, and read in parts of lines here, 3 us more.)
 template <int D, int ROWS>
 __global__ void __launch_bounds__(256) join_rows_kernel(const AttendArgs a, const JoinSpace space) {
   wait_for_previous();
