@@ -6,9 +6,10 @@
 // What bounds it: the two products, 4 d flops a row and key, and one power of two a row and key; at
 // d = 128 the tensor core, the special-function unit and the operands' way through shared memory
 // need the same time (2048 cycles for 256 rows and 128 keys), at d = 64 the powers of two do. The
-// rows' chain (scores, weights, sum) is what is left over: measured 1.13 ms for 2 x 2048 rows x 32
-// heads behind 14,336 keys at d = 128 (910 TFLOP/s, 0.55 of the measured bf16 rate; the tensor
-// core works 41 % of the time, the special-function unit 43 %).
+// rows' own work is what it comes to: measured 1.12 ms for 2 x 2048 rows x 32 heads behind 14,336
+// keys at d = 128 (920 TFLOP/s, 0.56 of the measured bf16 rate; the tensor core works 41 % of the
+// time, the special-function unit 43 %), 0.97 with the rows' work alone. Score columns for each half
+// of a key tile, so that scores never wait for weights, took 1.15 ms.
 //
 // One CTA a multiprocessor takes 256 query rows (two tiles of 128) of one key head and walks key
 // tiles of 128. Eight warps load codes to registers, widen them to halves (exact) and write them to

@@ -10,7 +10,7 @@
 // the scores of its keys), and values times weights. A weight is used as two halves, its rounding
 // and what that left (2^-22 of it together), which lie in neighbouring columns and are added at
 // the end: the output is as exact as one with fp32 weights at the cost of one product.
-// Measured: 2 x 8 x 16,384 queries of up to 96 of 16,384 keys, d = 64: 588 us (3.2 GB gathered, 5.5
+// Measured: 2 x 8 x 16,384 queries of up to 96 of 16,384 keys, d = 64: 590 us (3.2 GB gathered, 5.4
 // TB/s; 1.6 K warp instructions a query, 0.67 of the issue slots); 64 x 8 queries, d = 128: 10 us.
 // int8 scores by four-product integer instructions were slower (739 us: they issue at a fraction of
 // the products' rate), and so were fewer warps with more registers (692 us at 16 warps a
