@@ -163,7 +163,8 @@ ALHR_API size_t alhr_attend_cache_workspace(const alhr_cache* cache,
  * row's out and lse NaN and touches no other row. Rows outside every request keep what they hold.
  * seq_len is cut at max_blocks * block_size, q_start at [0, tokens]; keys in blocks outside
  * [0, blocks) are left out and set ALHR_DEVERR_BLOCK. Only table entries, scales and blocks that
- * hold visible keys are read, and codes behind seq_len have no effect.
+ * hold visible keys are read, and codes behind seq_len have no effect. A value scale below 2^-100
+ * (alhr_store_cache writes none) counts as 0.
  *   Q         device, type as given; base 16-byte aligned
  *   out       device [tokens][q_heads][d], type of Q, 16-byte aligned
  *   lse       device float [tokens][q_heads], or NULL

@@ -777,3 +777,89 @@ def test_step_captured_and_replayed(C):
         for s, o, (c, w) in zip((a, b), outs, want):
             assert torch.equal(o, w) and torch.equal(s["table"], c["table"])
             assert all(torch.equal(s["cache"][k], c["cache"][k]) for k in c["cache"])
+
+
+# ------------------------------------------------------------------ value scales of any size
+
+def spread_scales(s, powers):
+    """Block i of the cache has the value scale 2^powers[i % len]; None: 0, with its codes kept."""
+    c = s["cache"]
+    n = c["v_scale"].shape[0]
+    p = [powers[i % len(powers)] for i in range(n)]
+    f = torch.tensor([0.0 if x is None else 2.0 ** x for x in p], device="cuda")
+    c["v_scale"].copy_(f[:, None].expand_as(c["v_scale"]))
+    # blocks in the order of their positions, so that the powers follow one another in a sequence
+    for r in range(s["table"].shape[0]):
+        row = s["table"][r]
+        row.copy_(torch.where(row >= 0, row.masked_fill(row < 0, n).sort()[0], row))
+    return s
+
+
+@pytest.mark.parametrize("rows,keys,requests", [(1, 32768, 64), (4, 32768, 64), (300, 16384, 8)])
+def test_attend_lse_of_zero_values(C, rows, keys, requests):
+    """Heads whose values are all zero (a scale of 2^-100 as store_cache writes it, 0 as
+    alloc_cache does), with scores that rise by nearly 8 powers of two behind the first keys: lse is
+    that of the scores, out is zero. The requests share their pages."""
+    hkv, d, bs = 8, 64, 128
+    cache = C.alloc_cache(keys // bs, hkv, bs, d)
+    cache["v_scale"].fill_(2.0 ** -100)
+    cache["v_scale"][:, 0] = 0
+    cache["k_scale"].fill_(1.0)
+    cache["k"][..., 0] = 54
+    cache["k"][0, :, :, 0] = 0
+    q = torch.zeros(requests * rows, hkv, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    table = torch.arange(keys // bs, device="cuda").int().expand(requests, -1).contiguous()
+    got = C.attend_cache(q, cache, table, ints([keys - rows] * requests), ints([keys] * requests),
+                         ints([rows * i for i in range(requests + 1)]), max_q=rows, scale=0.1,
+                         want_lse=True)
+    seen = keys - rows + 1 + torch.arange(rows, device="cuda").double().repeat(requests)
+    want = torch.log(128 + (seen - 128) * math.exp(5.4))[:, None]
+    assert bool((got["out"] == 0).all())
+    # terms of at most 5.4 and their sum: a few roundings of each, the sum's of `keys` numbers in
+    # 32 bits at 2^-24 of it for each step of a lane's or thread's chain (at most keys / 16)
+    assert float((got["lse"].double() - want).abs().max()) <= keys / 16 * 2.0 ** -24 + 2.0 ** -18
+
+
+SPREADS = [
+    [-100, 20], [-100, 40], [20, -100], [30, -100, None, 0], [0, 60, -60, 90, -99, 3],
+    [-99, -60, -20, 20, 60, 100], [100, 60, 20, -20, -60, -99], [None, -6], [-6, None, -100],
+    [110, -100], [-33, 0], [0, 33, -33], [None], [-100], [-70, -66],
+]
+
+
+@pytest.mark.parametrize("powers", SPREADS, ids=str)
+@pytest.mark.parametrize("new,d,code", [([1, 1], 64, I8), ([3, 4], 128, E4), ([70, 130], 64, E4),
+                                        ([300, 9], 128, I8)])
+def test_attend_value_scales_of_any_size(C, powers, new, d, code):
+    """Blocks whose value scales lie any number of powers of two apart, zeros among them: every
+    key keeps its share of the softmax, whatever the scale of its value."""
+    s = spread_scales(make([1800, 330], new, 4, 2, d, 16, code, torch.bfloat16, qs=0.5), powers)
+    c, q = s["cache"], s["q"]
+    for scale in (None, 0.0):
+        check(C, s, scale=scale)
+        # without the absolute term that check allows for half-precision outputs: tiny values too
+        sc = 1 / math.sqrt(d) if scale is None else scale
+        ref, _, weight, most, _, small = attend_ref(q, c["k"], c["v"], c["k_scale"], c["v_scale"],
+                                                    s["table"], s["ctx"], s["seq"], s["start"], sc)
+        out = C.attend_cache(q, c, s["table"], s["ctx"], s["seq"], s["start"], max_q=s["max_q"],
+                             scale=scale)["out"]
+        tol = 2.0 ** -8 * ref.abs() + (2.0 ** -11 + 2 * score_error(d, most)) * weight * 1.01
+        assert bool(((out.double() - ref).abs() <= tol + 2.0 ** -25 * small).all())
+
+
+@pytest.mark.parametrize("new", [[1], [40]])
+def test_attend_zeros_beside_large_values(C, new):
+    """Every second block holds zeros, the other ones 2^30: equal scores, so out is their mean."""
+    n, bs, d = 4096, 64, 128
+    x = torch.zeros(n, 1, d, device="cuda")
+    x.view(n // bs, bs, d)[1::2] = 2.0 ** 30
+    cache = C.alloc_cache(n // bs, 1, bs, d)
+    C.store_cache(torch.zeros_like(x), x, cache, torch.arange(n, device="cuda"))
+    t = new[0]
+    q = torch.ones(t, 2, d, dtype=torch.bfloat16, device="cuda")
+    table = torch.arange(n // bs, device="cuda").int()[None]
+    got = C.attend_cache(q, cache, table, ints([n - 1] * 1), ints([n]), ints([0, t]), max_q=t,
+                         want_lse=True)
+    assert float((got["out"].double() / 2.0 ** 30 - 0.5).abs().max()) <= 2.0 ** -9
+    assert float((got["lse"] - math.log(n)).abs().max()) <= 1e-5

@@ -1,7 +1,8 @@
 // cache_chunk.cu -- attention of many query rows a request over all of its keys (prompts, chunks).
 //
 // Mathematics as in cache_decode.cu: x_j = s_j log2 e + log2 v_scale_j, weights 2^(x_j - M) times
-// value codes, l = sum w_j / v_scale_j.
+// value codes, l = sum w_j / v_scale_j, or from the scores alone behind a value scale that is not
+// between 2^-48 and 2^28.
 //
 // What bounds it: the two products, 4 d flops a row and key, and one power of two a row and key; at
 // d = 128 the tensor core, the special-function unit and the operands' way through shared memory
@@ -53,7 +54,9 @@ struct ChunkSmem {
   static constexpr int q = 0;                    // two tiles
   static constexpr int k = 2 * kTile;            // two tiles
   static constexpr int v = 4 * kTile;            // two tiles
-  static constexpr int scales = 6 * kTile;       // [4][8] of {k scale, log2 v scale, 1 / v scale}
+  // [4][8] of {k scale, log2 v scale, 1 / v scale}; {0, -infinity, 0} for a group that is not there,
+  // {k scale, infinity, log2 v scale} for one whose value scale is not near 1
+  static constexpr int scales = 6 * kTile;
   static constexpr int bars = scales + 4 * 8 * 16;
   static constexpr int misc = bars + 32 * 8;
   static constexpr int bytes = misc + 64;
@@ -363,6 +366,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint32_t s_col = tmem + lanes + i * 128, o_col = tmem + lanes + 256 + i * D;
     const unsigned char* scales = chunk_smem + L::scales;
     float m = -INFINITY, l = 0.f, qs = 0.f;
+    float rmax = 0.f;  // R, while `wide`
+    bool wide = false;
     int seen = 0, row = 0;  // columns < seen of the tile are visible
     // this row's queries to shared memory, scaled by a power of two so that halves hold them
     auto load_q = [&](const ChunkCursor& cur) {
@@ -436,7 +441,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         // ---- the unit before (or this piece of it) has ended, another one begins
         const ChunkCursor was = *cursor;
         const int was_row = row;
-        const float was_m = m, was_l = l;
+        const float was_l = l, was_r = wide ? rmax : m;
+        const float up = wide ? exp2_fast(m - rmax) : 1.f;
         const bool was_busy = busy, to_end = left == 0, started = from_start;
         if (j > 0 && tid == 0 && started && !to_end) {
           meta->r = was.r;
@@ -447,6 +453,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         first = true;
         fresh = false;
+        wide = false;
         if (j < count) {
           ChunkCursor now = was;
           if (j > 0) now = next_unit(a, cursor, row_limit);
@@ -477,7 +484,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const int tok = was_row / a.group;
           const long long at = static_cast<long long>(was.q.q_lo + tok) * a.q_heads +
                                was.h * a.group + (was_row - tok * a.group);
-          const float inv = was_l == 0.f ? 0.f : 1.f / was_l;  // no key; NaN stays
+          const float inv = was_l == 0.f ? 0.f : up / was_l;  // no key; NaN stays
           float* part = space.part + (static_cast<long long>(piece) * 2 + (started ? 1 : 0)) *
                                          (kRows * (D + 2));
           const int pr = i * 128 + rt;
@@ -499,18 +506,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
               }
             } else if (on) {
-              uint4* dst = reinterpret_cast<uint4*>(part + pr * D + c * 32);
+              float4* dst = reinterpret_cast<float4*>(part + pr * D + c * 32);
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                dst[k] = make_float4(__uint_as_float(v[4 * k]) * inv,
+                                     __uint_as_float(v[4 * k + 1]) * inv,
+                                     __uint_as_float(v[4 * k + 2]) * inv,
+                                     __uint_as_float(v[4 * k + 3]) * inv);
             }
           }
           if (on && whole) {
             if (a.lse)
-              a.lse[at] = was_l == 0.f ? -INFINITY : (was_m + log2f(was_l)) * 0.6931471805599453f;
+              a.lse[at] = was_l == 0.f ? -INFINITY : (was_r + log2f(was_l)) * 0.6931471805599453f;
           } else if (on) {
-            part[kRows * D + pr] = was_m;
-            part[kRows * D + kRows + pr] = was_l;
+            float r = was_r, sum = was_l;
+            settle(r, sum, kPartLog);
+            part[kRows * D + pr] = r;
+            part[kRows * D + kRows + pr] = sum;
           }
           __syncwarp();
           fence_before();
@@ -525,9 +537,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const float4* sc = reinterpret_cast<const float4*>(scales) + (j & 3) * 8;
         // Nearly always M stays as it is: weights are taken with it at once, and held until it is
         // known that none is above 2^15. The tile in which M has to grow, the first one of a unit
-        // and those that a mask cuts take two passes over the scores.
+        // and those that a mask cuts take two passes over the scores; so does one with a value
+        // scale that is not near 1 (its weights are infinite here), and every one behind it.
         bool done = false;
-        if (!first && !cut) {
+        if (!first && !cut && !wide) {
           uint32_t p[64];
           float sum = l, most = m == -INFINITY ? INFINITY : 0.f;
           uint32_t v[2][32];
@@ -573,7 +586,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         if (!done) {
           // by 32 columns: most of what a mask cuts is seen by the whole warp or by none of it
+          auto log_of = [](const float4& f) { return f.y == INFINITY ? f.z : f.y; };
           float top = -INFINITY;  // the largest x of the row
+          bool far = false;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             const int here = seen - c * 32;
@@ -592,8 +607,41 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
               for (int k = 1; k < 16; ++k) x = fmaxf(x, __uint_as_float(v[u * 16 + k]));
               const float4 f = sc[c * 2 + u];
+              far |= f.y == INFINITY;
               // -infinity stays where the factor is 0
-              top = fmaxf(top, x == -INFINITY ? x : fmaf(x, qs * f.x, f.y));
+              top = fmaxf(top, x == -INFINITY ? x : fmaf(x, qs * f.x, log_of(f)));
+            }
+          }
+          if (far && !wide) {
+            wide = true;
+            rmax = m;  // l is in units of 2^M so far
+            settle(rmax, l, 0);
+          }
+          if (wide) {  // l and R from the scores
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              const int here = seen - c * 32;
+              if (!__any_sync(0xffffffffu, here > 0)) break;
+              uint32_t v[32];
+              tmem_ld32(v, s_col + c * 32);
+              wait_ld();
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const float4 f = sc[c * 2 + u];
+                const int some = f.y == -INFINITY ? 0 : here - u * 16;  // a group that is not there
+                const float f1 = qs * f.x;
+                float x[16], most = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  x[k] = k < some ? __uint_as_float(v[u * 16 + k]) * f1 : -INFINITY;
+                  most = fmaxf(most, x[k]);
+                }
+                const float r = fmaxf(rmax, most), from = r == -INFINITY ? 0.f : r;
+                l *= exp2_fast(rmax - from);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) l += exp2_fast(x[k] - from);
+                rmax = r;
+              }
             }
           }
           const bool grow = top > m + kTopLog + 8.f;
@@ -601,7 +649,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const float mn = fmaxf(m, top - kTopLog);
             const float keep = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
             m = mn;
-            l *= keep;
+            if (!wide) l *= keep;
             if (!first) {
               // the product before this tile's scores is complete: they were issued after it
 #pragma unroll 1
@@ -636,7 +684,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               for (int u = 0; u < 2; ++u) {
                 const float4 f = sc[c * 2 + u];
                 // not 0: a masked score stays -infinity (the largest, 2^29, times 1e-37 is nothing)
-                const float f1 = fmaxf(qs * f.x, 1e-37f), f0 = f.y - base;
+                const float f1 = fmaxf(qs * f.x, 1e-37f), f0 = log_of(f) - base;
                 float part = 0.f;
 #pragma unroll
                 for (int k = 0; k < 16; k += 2) {
@@ -645,7 +693,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                   part += x0 + x1;
                   p[u * 8 + k / 2] = pack2(x0, x1, true);
                 }
-                l = fmaf(part, f.z, l);
+                if (!wide) l = fmaf(part, f.z, l);
               }
             }
             tmem_st16(s_col + c * 16, p);  // over scores that have been read
@@ -748,8 +796,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                          : "memory");
           }
         if (keys && lane < 2) {
-          const float v1 = fmaxf(vs, kTinyScale);
-          float4 f = make_float4(ks, __log2f(v1), __frcp_rn(v1), 0.f);
+          const float log_v = vs >= kTinyScale ? __log2f(vs) : -INFINITY;
+          float4 f = make_float4(ks, log_v, __frcp_rn(vs), 0.f);
+          if (!is_near(vs)) f = make_float4(ks, INFINITY, log_v, 0.f);
           if (!there) f = make_float4(0.f, -INFINITY, 0.f, 0.f);
           // four tiles of scales: the rows are done with those of tile j - 3 before the scores of
           // tile j - 2 are asked for, which the wait above has seen

@@ -5,7 +5,10 @@
 // l = sum w_j / v_scale_j is the softmax's sum: out = O / l. Taking the block's value scale into
 // the exponent keeps the weights of blocks with very different scales in the range of a half: M is
 // chosen so that the largest weight lies in [2^7, 2^15], and weights down to 2^-21 of it are
-// rounded at 2^-11 of themselves. l is summed from the fp32 weights.
+// rounded at 2^-11 of themselves. l is summed from the fp32 weights. That holds while all value
+// scales are between 2^-48 and 2^28; from the first tile on that has another one (zeros are stored
+// with 2^-100) the unit sums l = sum 2^(s_j log2 e - R) from the scores, R their running maximum, and
+// out = 2^(M - R) O / l: a head of zeros takes the second power of two for every key.
 //
 // What bounds it: the codes have to be read once, 2 d bytes a key and head; everything else is
 // there to keep the memory busy (64 sequences of up to 16,384 int8 keys, 32 query heads over 8, d =
@@ -228,9 +231,12 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
   float qscale[NT][2];  // factor of the scores of columns 2 t, 2 t + 1
   int see[NT][2];       // visible keys of those columns' rows
   float o[NT][KS][4], m[NT][2], l[NT][2];
+  float rmax[NT][2];    // R, while `wide`
+  bool wide = false;
   int see_min;
   auto begin_unit = [&]() {
     const int row0 = cur.group * ROWS;
+    wide = false;
     see_min = 0x7fffffff;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -289,6 +295,33 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
     see_min = __reduce_min_sync(0xffffffffu, see_min);
   };
 
+  // l and R of a tile from its scores, where the value scales are far apart
+  auto sum_scores = [&](const float (&s)[SUBS][NT][4], uint32_t scales, int key0) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float x[SUBS][2], top = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < SUBS; ++u) {
+          const uint4 sc = lds128(scales + u * 16);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const bool on = sc.z && key0 + u * 16 + key_of(g) + i * 2 < see[n][c];
+            x[u][i] = on ? s[u][n][2 * i + c] * (qscale[n][c] * __uint_as_float(sc.x)) : -INFINITY;
+            top = fmaxf(top, x[u][i]);
+          }
+        }
+        const float r = fmaxf(rmax[n][c], group_max(top));
+        const float from = r == -INFINITY ? 0.f : r;
+        float sum = l[n][c] * exp2_fast(rmax[n][c] - from);
+#pragma unroll
+        for (int u = 0; u < SUBS; ++u) sum += exp2_fast(x[u][0] - from) + exp2_fast(x[u][1] - from);
+        l[n][c] = sum;
+        rmax[n][c] = r;
+      }
+  };
+
   // column c of column group n: row, sums over the keys of all lanes
   auto end_unit = [&](bool from_start, bool to_end) {
     const int row0 = cur.group * ROWS;
@@ -299,9 +332,11 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
         const float sum_l = group_add(l[n][c]);
         const int col = n * 8 + 2 * t + c, row = row0 + col;
         if (row >= cur.q.rows) continue;
+        const float base = wide ? rmax[n][c] : m[n][c];
+        // no key; NaN stays
+        const float inv = sum_l == 0.f ? 0.f : (wide ? exp2_fast(m[n][c] - base) : 1.f) / sum_l;
         // numbers 16 k + g and 16 k + 8 + g of the row
         if (from_start && to_end) {
-          const float inv = sum_l == 0.f ? 0.f : 1.f / sum_l;  // no key; NaN stays
           const int tok = row / a.group;
           const long long at = static_cast<long long>(cur.q.q_lo + tok) * a.q_heads +
                                cur.h * a.group + (row - tok * a.group);
@@ -313,7 +348,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
             p[16 * k + 8] = static_cast<uint16_t>(w >> 16);
           }
           if (a.lse && g == 0)
-            a.lse[at] = sum_l == 0.f ? -INFINITY : (m[n][c] + log2f(sum_l)) * 0.6931471805599453f;
+            a.lse[at] = sum_l == 0.f ? -INFINITY : (base + log2f(sum_l)) * 0.6931471805599453f;
         } else {
           float* const part = space.part +
                               (static_cast<long long>(piece) * 2 + (from_start ? 1 : 0)) *
@@ -321,12 +356,14 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
           float* const p = part + col * D + g;
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
-            p[16 * k] = o[n][k][c];
-            p[16 * k + 8] = o[n][k][2 + c];
+            p[16 * k] = o[n][k][c] * inv;
+            p[16 * k + 8] = o[n][k][2 + c] * inv;
           }
           if (g == 0) {
-            part[ROWS * D + col] = m[n][c];
-            part[ROWS * D + ROWS + col] = sum_l;
+            float r = base, sum = sum_l;
+            settle(r, sum, kPartLog);
+            part[ROWS * D + col] = r;
+            part[ROWS * D + ROWS + col] = sum;
           }
         }
       }
@@ -350,7 +387,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
     const uint32_t base = ring + stage * Tile<D>::kStride;
     // scores
     float s[SUBS][NT][4];
-    float add[SUBS], inv_vs[SUBS];
+    float add[SUBS], inv_vs[SUBS], ks[SUBS];
+    bool far = false;
 #pragma unroll
     for (int u = 0; u < SUBS; ++u) {
 #pragma unroll
@@ -375,19 +413,45 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
         for (int n = 0; n < NT; ++n) mma16816(s[u][n], a0, a1, a2, a3, qf[n][k][0], qf[n][k][1]);
       }
       const uint4 sc = lds128(base + kStageBytes + u * 16);
-      const float vs = fmaxf(__uint_as_float(sc.y), kTinyScale);
-      add[u] = sc.z ? __log2f(vs) : -INFINITY;
-      inv_vs[u] = sc.z ? rcp_fast(vs) : 0.f;
+      const float v = __uint_as_float(sc.y);
+      ks[u] = __uint_as_float(sc.x);
+      add[u] = sc.z ? __log2f(v) : -INFINITY;
+      inv_vs[u] = sc.z ? rcp_fast(v) : 0.f;
+      far |= sc.z && !is_near(v);
+    }
+    const int key0 = cur.tile * Tile<D>::kKeys;
+    if (wide || far) {
+      if (!wide) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {  // l is in units of 2^M so far
+            l[n][c] = group_add(l[n][c]);
+            rmax[n][c] = m[n][c];
+            settle(rmax[n][c], l[n][c], 0);
+            if (g) l[n][c] = 0.f;
+          }
+        wide = true;
+      }
+      sum_scores(s, base + kStageBytes, key0);
+#pragma unroll
+      for (int u = 0; u < SUBS; ++u) {
+        const uint4 sc = lds128(base + kStageBytes + u * 16);
+        const float v = __uint_as_float(sc.y);
+        add[u] = sc.z && v >= kTinyScale ? __log2f(v) : -INFINITY;
+        inv_vs[u] = 0.f;  // l is complete
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < SUBS; ++u)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float f1 = qscale[n][c] * __uint_as_float(sc.x);
+          const float f1 = qscale[n][c] * ks[u];
           s[u][n][c] = fmaf(s[u][n][c], f1, add[u]);
           s[u][n][2 + c] = fmaf(s[u][n][2 + c], f1, add[u]);
         }
-    }
-    const int key0 = cur.tile * Tile<D>::kKeys;
     if (key0 + Tile<D>::kKeys > see_min) {  // some row does not see the whole tile
 #pragma unroll
       for (int u = 0; u < SUBS; ++u) {
@@ -421,7 +485,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1)
           const float mn = fmaxf(m[n][c], group_max(x) - kTopLog);
           const float keep = mn == -INFINITY ? 1.f : exp2_fast(m[n][c] - mn);
           m[n][c] = mn;
-          l[n][c] *= keep;
+          if (!wide) l[n][c] *= keep;
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
             o[n][k][c] *= keep;

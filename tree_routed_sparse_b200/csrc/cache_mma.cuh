@@ -98,7 +98,19 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// The smallest value scale that weights are formed with: log2 of a scale of 0 has to stay finite.
+// ---- value scales in the exponent (cache_decode.cu, cache_chunk.cu)
+// Value scales below this count as 0: such a key has its share of the softmax and no value.
 constexpr float kTinyScale = 7.888609052e-31f;  // 2^-100
+// Where all value scales of a unit are inside these bounds, the sum of its weights over the scales is
+// below 2^(15 + 48) for each of up to 2^30 keys, and what it loses of weights below 2^-126 is 2^(-126
+// + 48) a key against 2^(7 - 28) for the key that set M: nothing that 32 bits hold.
+constexpr float kNearLow = 3.552713678800501e-15f, kNearHigh = 268435456.f;  // 2^-48, 2^28
+__device__ __forceinline__ bool is_near(float v_scale) {
+  return v_scale >= kNearLow && v_scale <= kNearHigh;
+}
+
+__device__ __forceinline__ float power_of_two(int e) {  // -126 <= e <= 127
+  return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+}
 
 }  // namespace alhr

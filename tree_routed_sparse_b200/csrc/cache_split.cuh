@@ -77,9 +77,22 @@ struct JoinMeta {
 
 struct JoinSpace {
   JoinMeta* meta;  // [pieces]
-  float* part;     // [pieces][2] of O [ROWS][D], M [ROWS], l [ROWS]: of a unit that began in an
+  float* part;     // [pieces][2] of y [ROWS][D], R [ROWS], l [ROWS]: of a unit that began in an
                    // earlier piece, of one that begins here
 };
+
+// l 2^r with l in [2^to, 2^(to + 1)).
+__device__ __forceinline__ void settle(float& r, float& l, int to) {
+  if (l > 0.f) {  // not 0 (no key), not NaN
+    const int k = min(static_cast<int>(__float_as_uint(l) >> 23) - 127 - to, 126);
+    l *= power_of_two(-k);
+    r += static_cast<float>(k);
+  }
+}
+// A piece leaves its own answer y = sum p v / sum p, and sum p = l 2^R with l about 2^-12: the weights
+// l_i 2^(R_i - max R) of up to 2^11 pieces add up to no more than 1, so that the sum of y_i times
+// weight is in range where the values are.
+constexpr int kPartLog = -12;
 
 inline size_t join_bytes(int pieces, int rows, int d) {
   return static_cast<size_t>(pieces) * (32 + 2 * static_cast<size_t>(rows) * (d + 2) * sizeof(float));
@@ -119,7 +132,7 @@ constexpr int kJoinWarps = 8;
 
 // Joins the partial sums of the units that span pieces, one CTA for each piece in which such a unit
 // begins. Up to eight warps share a row: each joins every k-th partial (the lanes take 32 weights
-// 2^(M_i - max M) at a time, so that the loads of the sums do not wait for one another), then their
+// l_i 2^(R_i - max R) at a time, so that the loads of y do not wait for one another), then their
 // sums are added in the order of the warps.
 template <int D, int ROWS>  // ROWS <= 16
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendArgs a,
@@ -152,8 +165,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendArgs 
       float f = 0.f;
       if (i0 + lane < mine) {
         const float* x = part(sub + (i0 + lane) * shared_by) + ROWS * D + r;
-        f = exp2_fast(x[0] - base);
-        l = fmaf(x[ROWS], f, l);
+        f = exp2_fast(x[0] - base) * x[ROWS];
+        l += f;
       }
       const int some = min(32, mine - i0);
 #pragma unroll 8
@@ -206,10 +219,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendArgs 
 }
 
 // The same for units of many rows, of which most span two or three pieces: a thread takes four
-// numbers of two rows through all partials, with a running M, so that a row costs two dependent
+// numbers of two rows through all partials, with a running max R, so that a row costs two dependent
 // trips to memory (the unit, its partials) and all rows of a CTA make them together: 9 us for 144
 // units of 256 rows in 31 tiles a piece, d = 64, where a warp for each pair of rows took 20 and two
-// passes over the partials 12. (O with the rows innermost would be written in whole lines, 1 us less
+// passes over the partials 12. (y with the rows innermost would be written in whole lines, 1 us less
 // in a chunk's CTAs, and read in parts of lines here, 3 us more.)
 template <int D, int ROWS>
 __global__ void __launch_bounds__(256) join_rows_kernel(const AttendArgs a, const JoinSpace space) {
@@ -240,9 +253,9 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const AttendArgs a, cons
       const float4 y = *reinterpret_cast<const float4*>(x + row * D + col);
       const float mi = x[ROWS * D + row], li = x[ROWS * D + ROWS + row];
       const float mn = fmaxf(m[k], mi), base = mn == -INFINITY ? 0.f : mn;
-      const float keep = exp2_fast(m[k] - base), w = exp2_fast(mi - base);
+      const float keep = exp2_fast(m[k] - base), w = exp2_fast(mi - base) * li;
       m[k] = mn;
-      l[k] = fmaf(li, w, l[k] * keep);
+      l[k] = fmaf(l[k], keep, w);
       acc[k][0] = fmaf(y.x, w, acc[k][0] * keep);
       acc[k][1] = fmaf(y.y, w, acc[k][1] * keep);
       acc[k][2] = fmaf(y.z, w, acc[k][2] * keep);
