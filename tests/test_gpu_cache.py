@@ -1,5 +1,8 @@
 """The paged 8-bit cache against its definition in 64 bits (tests/cache_util.py)."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -9,6 +12,7 @@ from cache_util import (SAT, attend_ref, ceil_div, numbers, plan_ref, random_cac
 
 pytestmark = pytest.mark.gpu
 I8, E4 = torch.int8, torch.float8_e4m3fn
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -88,6 +92,26 @@ def test_plan_many(C, r, top):
     for key, w in zip(("q_start", "seq_len", "slots", "positions"), want):
         assert got[key].tolist() == w, key
     assert tab.tolist() == want[5] and got["free_next"].item() == want[4] and err.item() == 0
+
+
+@pytest.mark.parametrize("counts", [[6127, 6128, 6143, 6144, 8192, 6127], [6143], [8192, 6144]])
+def test_plan_at_the_edge_of_the_default_shared_memory(counts):
+    """Request counts whose sums fill what a kernel gets of shared memory without asking, in a
+    process of their own: an earlier, larger call leaves the limit raised."""
+    code = f"""
+import sys
+sys.path[:0] = ["tests", "."]
+import torch
+from tree_routed_sparse_b200 import cache as C
+ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+for r in {counts}:
+    got = C.plan_blocks(ints([0] * r), ints([1] * r), torch.full((r, 1), -1, dtype=torch.int32,
+                        device="cuda"), ints(list(range(r))), ints([0]), r, 16)
+    assert got["slots"].tolist() == [16 * i for i in range(r)], r
+"""
+    done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True,
+                          timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 def test_plan_without_requests(C):

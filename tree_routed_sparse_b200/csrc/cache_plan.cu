@@ -159,7 +159,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_blocks_kernel(const PlanArg
 
 cudaError_t launch_plan_blocks(const PlanArgs& a, cudaStream_t st) {
   const int smem = (2 * a.requests + 1) * static_cast<int>(sizeof(int));
-  if (smem > 48 * 1024) {
+  // the limit without asking counts what the kernel declares itself (block_exclusive's sums) too
+  constexpr int kDeclared = kPlanThreads / 32 * static_cast<int>(sizeof(long long));
+  if (smem + kDeclared > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(
         plan_blocks_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
