@@ -3,6 +3,7 @@ import math
 import os
 import subprocess
 import sys
+import threading
 
 import pytest
 import torch
@@ -112,6 +113,40 @@ for r in {counts}:
     done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True,
                           timeout=300)
     assert done.returncode == 0, done.stderr[-2000:]
+
+
+def test_plan_from_two_threads(C):
+    """Plans of different sizes from host threads with streams of their own: none changes what
+    another one's kernel is launched with."""
+    faults = []
+
+    def work(r):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                args = (ints([0] * r), ints([1] * r),
+                        torch.full((r, 1), -1, dtype=torch.int32, device="cuda"),
+                        ints(list(range(r))), ints([0]))
+                q, seq, nxt = ints([0] * (r + 1)), ints([0] * r), ints([0])
+                slots, pos = torch.zeros(r, dtype=torch.int64, device="cuda"), ints([0] * r)
+                torch.cuda.current_stream().synchronize()
+                L, st = alhr.lib(), torch.cuda.current_stream().cuda_stream
+                ptr = [x.data_ptr() for x in (*args, q, seq, slots, pos, nxt)]
+                for _ in range(2000):
+                    got = L.alhr_plan_blocks(r, 1, 16, r, r, r, *ptr, None, st)
+                    assert got == 0, (r, got)
+                torch.cuda.current_stream().synchronize()
+                assert slots.tolist() == [16 * i for i in range(r)]
+        except Exception as e:  # noqa: BLE001 - handed to the test
+            faults.append(e)
+
+    from tree_routed_sparse_b200 import alhr
+    threads = [threading.Thread(target=work, args=(r,)) for r in (8192, 6200, 8192, 6200)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not faults, faults[0]
 
 
 def test_plan_without_requests(C):

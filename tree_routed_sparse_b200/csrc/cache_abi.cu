@@ -9,7 +9,7 @@
 
 namespace {
 
-constexpr int kMaxRequests = 8192;  // the plan keeps two words a request in shared memory
+using alhr::kMaxRequests;
 constexpr int kMaxGroup = 64;
 constexpr int kMaxHeads = 65535;           // a grid's second axis
 constexpr int64_t kMaxLength = 1 << 30;    // tokens of a block table's row: sums of two stay 32 bits

@@ -8,6 +8,8 @@
 
 namespace alhr {
 
+constexpr int kMaxRequests = 8192;  // the plan keeps two words a request in shared memory
+
 struct PlanArgs {
   int requests, max_blocks, block_size, blocks, tokens, free_count;
   const int32_t* ctx_len;

@@ -57,6 +57,11 @@ __device__ __forceinline__ long long block_exclusive(long long v, long long* all
   return before + s - v;
 }
 
+// Two words a request and the end of the last one.
+constexpr int plan_smem_bytes(int requests) {
+  return (2 * requests + 1) * static_cast<int>(sizeof(int));
+}
+
 __global__ void __launch_bounds__(kPlanThreads) plan_blocks_kernel(const PlanArgs a) {
   extern __shared__ int plan_smem[];
   int* start = plan_smem;                   // [requests + 1]
@@ -158,20 +163,23 @@ __global__ void __launch_bounds__(kPlanThreads) plan_blocks_kernel(const PlanArg
 }  // namespace
 
 cudaError_t launch_plan_blocks(const PlanArgs& a, cudaStream_t st) {
-  const int smem = (2 * a.requests + 1) * static_cast<int>(sizeof(int));
-  // the limit without asking counts what the kernel declares itself (block_exclusive's sums) too
-  constexpr int kDeclared = kPlanThreads / 32 * static_cast<int>(sizeof(long long));
-  if (smem + kDeclared > 48 * 1024) {
+  // One limit for every call, whatever its size: it belongs to the kernel, not to the call, and
+  // another thread may be between its own limit and its launch.
+  static thread_local bool configured[128] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 128 || !configured[dev]) {
     const cudaError_t e = cudaFuncSetAttribute(
-        plan_blocks_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        plan_blocks_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, plan_smem_bytes(kMaxRequests));
     if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 128) configured[dev] = true;
   }
   // a CTA for every 1024 rows or 64 requests
   const long long by_rows = (static_cast<long long>(a.tokens) + 1023) / 1024;
   const long long by_requests = (a.requests + 63) / 64;
   const int grid = static_cast<int>(
       max(1LL, min(148LL, by_rows > by_requests ? by_rows : by_requests)));
-  plan_blocks_kernel<<<grid, kPlanThreads, smem, st>>>(a);
+  plan_blocks_kernel<<<grid, kPlanThreads, plan_smem_bytes(a.requests), st>>>(a);
   return cudaGetLastError();
 }
 
