@@ -4,7 +4,6 @@
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include "cache_internal.h"
@@ -18,22 +17,6 @@ __device__ __forceinline__ long long block_row(const CacheView& c, int block, in
 
 __device__ __forceinline__ void cache_flag(uint32_t* dev_err, uint32_t bit) {
   if (dev_err) atomicOr(dev_err, bit);
-}
-
-// Code <-> number. CODE is an alhr_code.
-template <int CODE>
-__device__ __forceinline__ float decode(uint8_t c) {
-  if constexpr (CODE == ALHR_CODE_INT8) return static_cast<float>(static_cast<int8_t>(c));
-  else return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
-}
-
-template <int CODE>
-__device__ __forceinline__ uint8_t encode(float x) {  // to nearest even, saturated; NaN as 0
-  if (x != x) return 0;
-  if constexpr (CODE == ALHR_CODE_INT8)
-    return static_cast<uint8_t>(__float2int_rn(fminf(fmaxf(x, -127.f), 127.f)));
-  else
-    return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
 }
 
 // Eight consecutive numbers of type T (an alhr_type) as fp32.

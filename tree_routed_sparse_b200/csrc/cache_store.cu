@@ -12,6 +12,8 @@
 // rest are read again (from L2). The quotient x / s is one rounding of the exact one, by Markstein's correction
 // of x * (1 / s) (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
 // processor", 1990): three operations where a division takes about ten.
+#include <cuda_fp8.h>
+
 #include "cache_mma.cuh"
 
 namespace alhr {
