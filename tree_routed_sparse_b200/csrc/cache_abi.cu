@@ -247,8 +247,6 @@ alhr_status alhr_attend_cache_selected(const alhr_cache* cache,
   if (!Q || !block_table || !ctx_len || !seq_len || !idx || !count || !out)
     return ALHR_ERR_INVALID_ARG;
   if (!aligned16(Q) || !aligned16(out)) return ALHR_ERR_INVALID_ARG;
-  const int sms = multiprocessors();
-  if (!sms) return ALHR_ERR_CUDA;
   alhr::SelectArgs a{};
   a.c = view_of(cache);
   a.q = Q; a.out = out; a.table = block_table; a.ctx_len = ctx_len; a.seq_len = seq_len;
@@ -258,8 +256,8 @@ alhr_status alhr_attend_cache_selected(const alhr_cache* cache,
   a.rows = q.batch * q.q_heads * q.nq;
   a.scale_log2 = log2_scale(q.scale);
   a.dev_err = dev_err;
-  return from_cuda(alhr::launch_attend_selected(a, cache->d, cache->code, sms,
-                                                static_cast<cudaStream_t>(stream)));
+  return from_cuda(
+      alhr::launch_attend_selected(a, cache->d, cache->code, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -94,6 +94,6 @@ size_t chunk_workspace(int sms, int d);
 cudaError_t launch_chunk(const AttendArgs& a, int d, int code, int sms, int row_limit,
                          cudaStream_t st);
 cudaError_t launch_chunk_join(const AttendArgs& a, int d, int sms, cudaStream_t st);
-cudaError_t launch_attend_selected(const SelectArgs& a, int d, int code, int sms, cudaStream_t st);
+cudaError_t launch_attend_selected(const SelectArgs& a, int d, int code, cudaStream_t st);
 
 }  // namespace alhr

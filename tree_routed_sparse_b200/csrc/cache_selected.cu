@@ -253,7 +253,7 @@ cudaError_t selected_as(const SelectArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_attend_selected(const SelectArgs& a, int d, int code, int, cudaStream_t st) {
+cudaError_t launch_attend_selected(const SelectArgs& a, int d, int code, cudaStream_t st) {
   if (d == 64)
     return code == ALHR_CODE_INT8 ? selected_as<64, ALHR_CODE_INT8>(a, st)
                                   : selected_as<64, ALHR_CODE_E4M3>(a, st);
