@@ -125,10 +125,12 @@ alhr_status alhr_plan_blocks(int32_t requests, int32_t max_blocks, int32_t block
   // every CTA reads these while another one may have written its outputs already
   if (free_next == free_first || (requests > 0 && (seq_len == ctx_len || seq_len == new_len)))
     return ALHR_ERR_INVALID_ARG;
+  const int sms = multiprocessors();
+  if (!sms) return ALHR_ERR_CUDA;
   const alhr::PlanArgs a{requests, max_blocks, block_size, blocks,  tokens,  free_count,
                          ctx_len,  new_len,    block_table, free_blocks, free_first, q_start,
                          seq_len,  slots,      positions,  free_next, dev_err};
-  return from_cuda(alhr::launch_plan_blocks(a, static_cast<cudaStream_t>(stream)));
+  return from_cuda(alhr::launch_plan_blocks(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 alhr_status alhr_store_cache(const alhr_cache* cache, const void* K, const void* V, int32_t type,

@@ -81,7 +81,7 @@ struct SelectArgs {
   uint32_t* dev_err;
 };
 
-cudaError_t launch_plan_blocks(const PlanArgs& a, cudaStream_t st);
+cudaError_t launch_plan_blocks(const PlanArgs& a, int sms, cudaStream_t st);
 cudaError_t launch_store_cache(const StoreArgs& a, int d, int code, int type, cudaStream_t st);
 cudaError_t launch_load_cache(const LoadArgs& a, int d, int code, int type, cudaStream_t st);
 size_t attend_cache_workspace(int sms, int d, long long max_rows);

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_blocks_kernel(const PlanArg
 
 }  // namespace
 
-cudaError_t launch_plan_blocks(const PlanArgs& a, cudaStream_t st) {
+cudaError_t launch_plan_blocks(const PlanArgs& a, int sms, cudaStream_t st) {
   // One limit for every call, whatever its size: it belongs to the kernel, not to the call, and
   // another thread may be between its own limit and its launch.
   static thread_local bool configured[128] = {};
@@ -174,11 +174,11 @@ cudaError_t launch_plan_blocks(const PlanArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 128) configured[dev] = true;
   }
-  // a CTA for every 1024 rows or 64 requests
+  // a CTA for every 1024 rows or 64 requests, at most one a multiprocessor
   const long long by_rows = (static_cast<long long>(a.tokens) + 1023) / 1024;
   const long long by_requests = (a.requests + 63) / 64;
   const int grid = static_cast<int>(
-      max(1LL, min(148LL, by_rows > by_requests ? by_rows : by_requests)));
+      max(1LL, min(static_cast<long long>(sms), by_rows > by_requests ? by_rows : by_requests)));
   plan_blocks_kernel<<<grid, kPlanThreads, plan_smem_bytes(a.requests), st>>>(a);
   return cudaGetLastError();
 }
