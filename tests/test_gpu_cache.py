@@ -221,6 +221,60 @@ def test_store_bits(C, dtype, src, name, d, bs, heads):
         assert float(torch.where(on, 0.0, back[key]).abs().max()) == 0
 
 
+def large_store(kind, bs, g):
+    """(spec of runs, blocks) of a store whose warps look through 16 tokens each: prompts of ragged
+    lengths behind part-filled blocks, or single tokens; rows without a slot among them."""
+    spec, page = [], 0
+    rand = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))
+    while sum(n for *_, n in spec) < 1100:
+        if rand(0, 9) == 0:
+            spec.append((-1, 0, rand(1, 3 if kind == "single" else 40)))
+        if kind == "single":
+            spec.append((page, rand(0, bs - 1), 1))
+        else:
+            off, left = rand(0, bs - 1), rand(1, 5 * bs if kind == "long" else bs + 9)
+            while left:
+                n = min(left, bs - off)
+                spec.append((page, off, n))
+                page, off, left = page + 1, 0, left - n
+        page += 1 + (rand(0, 3) == 0)
+    # pages that follow one another in the call lie anywhere in the cache, some side by side
+    order = torch.randperm(page // 2, generator=g).tolist()
+    where = [2 * order[p // 2] + p % 2 if p // 2 < len(order) else p for p in range(page)]
+    return [(p if p < 0 else where[p], o, n) for p, o, n in spec], page + 1
+
+
+@pytest.mark.parametrize("kind,bs,d,dtype,src", [
+    ("long", 128, 128, E4, torch.bfloat16), ("long", 64, 64, I8, torch.float32),
+    ("long", 16, 128, I8, torch.float16), ("short", 32, 64, E4, torch.float32),
+    ("short", 128, 64, I8, torch.bfloat16), ("single", 16, 64, E4, torch.float16),
+    ("single", 128, 128, I8, torch.bfloat16)])
+def test_store_bits_of_many_tokens(C, kind, bs, d, dtype, src):
+    """Stores of more than 16,384 (token, head, keys or values) triples, of which a warp takes all
+    runs that begin in 16 tokens: several of them, and runs that go on past its 32 lanes."""
+    g = torch.Generator().manual_seed(len(kind) + bs + d)
+    heads = 8
+    spec, blocks = large_store(kind, bs, g)
+    slots = runs(spec, blocks, bs)
+    t = slots.numel()
+    assert t * heads * 2 > 16384 and len({p for p, *_ in spec if p >= 0}) == sum(p >= 0 for p, *_ in spec)
+    gg = torch.Generator(device="cuda").manual_seed(7)
+    cache = random_cache(blocks, heads, bs, d, dtype, gg, "cuda")
+    x = torch.randn(t, 2 * heads, d, generator=gg, device="cuda")
+    x *= torch.where(torch.arange(t, device="cuda") % 5 == 0, 6.0, 1.0)[:, None, None]
+    x = x.to(src)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ref = {}
+    for key, y in (("k", x[:, :heads]), ("v", x[:, heads:])):
+        codes, scale = cache[key].cpu().clone(), cache[key + "_scale"].cpu().clone()
+        store_ref(y.float().cpu(), codes, scale, slots)
+        ref[key], ref[key + "_scale"] = codes, scale
+    C.store_cache(x[:, :heads], x[:, heads:], cache, slots.cuda(), dev_err=err)
+    for key in ("k_scale", "v_scale", "k", "v"):
+        assert torch.equal(bits(cache[key].cpu()), bits(ref[key])), key
+    assert err.item() == 0
+
+
 @pytest.mark.parametrize("dtype", [I8, E4])
 def test_store_special_values(C, dtype):
     """Zeros, tiny and huge numbers, infinities and NaN; NaN in rows without a slot is not read."""
