@@ -976,3 +976,31 @@ def test_attend_zeros_beside_large_values(C, new):
                          want_lse=True)
     assert float((got["out"].double() / 2.0 ** 30 - 0.5).abs().max()) <= 2.0 ** -9
     assert float((got["lse"] - math.log(n)).abs().max()) <= 1e-5
+
+
+@pytest.mark.parametrize("powers", [[-6, -6, -6, -100], [-50, 3, 40], [-100, 40, -6, None]], ids=str)
+@pytest.mark.parametrize("requests,ctx,new,d", [(40, 3000, 1, 64), (6, 4000, 260, 128),
+                                                (6, 4000, 260, 64)])
+def test_attend_value_scales_of_many_units(C, powers, requests, ctx, new, d):
+    """Warps and CTAs that go through several requests and heads: what one unit's value scales ask
+    for ends with it."""
+    s = make([ctx + 37 * i for i in range(requests)], [new] * requests, 8, 8, d, 64, I8,
+             torch.bfloat16, qs=0.5)
+    s = spread_scales(s, powers)
+    s["cache"]["v_scale"][:, ::2] = 0.02  # every second head is an ordinary one
+    check(C, s)
+
+
+@pytest.mark.parametrize("requests,new", [(1500, [1]), (3000, [1, 0, 2, 40, 1])])
+def test_attend_many_requests(C, requests, new):
+    """More requests than threads of a CTA: each sums a run of them for the list of tiles."""
+    g = torch.Generator().manual_seed(requests)
+    ctx = torch.randint(0, 90, (requests,), generator=g).tolist()
+    check(C, make(ctx, [new[i % len(new)] for i in range(requests)], 2, 1, 64, 16, I8,
+                  torch.bfloat16, pad=3))
+
+
+def test_attend_without_rows(C):
+    """Requests without a row, and rows that belong to none: nothing is written."""
+    s = make([20, 3], [0, 0], 4, 2, 64, 16, I8, torch.bfloat16, pad=50)
+    check(C, s, max_q=None)
