@@ -55,7 +55,7 @@ struct ChunkSmem {
   static constexpr int k = 2 * kTile;            // two tiles
   static constexpr int v = 4 * kTile;            // two tiles
   // [4][8] of {k scale, log2 v scale, 1 / v scale}; {0, -infinity, 0} for a group that is not there,
-  // {k scale, infinity, log2 v scale} for one whose value scale is not near 1
+  // -infinity in the last place for one whose value scale is not near 1
   static constexpr int scales = 6 * kTile;
   static constexpr int bars = scales + 4 * 8 * 16;
   static constexpr int misc = bars + 32 * 8;
@@ -155,6 +155,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t (&v)[32], uint32_t addr) {
       : "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t (&v)[16], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];\n"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(addr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
@@ -173,6 +183,33 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+
+// {R, l} of a row with the scores of one tile.
+__device__ __forceinline__ float2 sum_scores(const float4* sc, uint32_t s_col, int seen, float qs,
+                                             float rmax, float l) {
+#pragma unroll 1
+  for (int u = 0; u < 8; ++u) {
+    const float4 f = sc[u];
+    const int here = f.z == 0.f ? 0 : seen - u * 16;  // 0: a group that is not there
+    uint32_t v[16];
+    tmem_ld16(v, s_col + u * 16);
+    wait_ld();
+    const float f1 = qs * f.x;
+    float most = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float x = k < here ? __uint_as_float(v[k]) * f1 : -INFINITY;
+      v[k] = __float_as_uint(x);
+      most = fmaxf(most, x);
+    }
+    const float r = fmaxf(rmax, most), from = r == -INFINITY ? 0.f : r;
+    l *= exp2_fast(rmax - from);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) l += exp2_fast(__uint_as_float(v[k]) - from);
+    rmax = r;
+  }
+  return make_float2(rmax, l);
 }
 
 // Two fp32 numbers an instruction.
@@ -538,7 +575,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         // Nearly always M stays as it is: weights are taken with it at once, and held until it is
         // known that none is above 2^15. The tile in which M has to grow, the first one of a unit
         // and those that a mask cuts take two passes over the scores; so does one with a value
-        // scale that is not near 1 (its weights are infinite here), and every one behind it.
+        // scale that is not near 1 (it makes the sum -infinity or NaN), and every one behind it.
         bool done = false;
         if (!first && !cut && !wide) {
           uint32_t p[64];
@@ -572,7 +609,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               sum = fmaf(lo, f.z, sum);
             }
           }
-          done = __all_sync(0xffffffffu, most <= 32768.f);
+          done = __all_sync(0xffffffffu, most <= 32768.f && sum >= 0.f);
           if (done) {
             l = sum;
             uint32_t half[32];
@@ -586,7 +623,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         if (!done) {
           // by 32 columns: most of what a mask cuts is seen by the whole warp or by none of it
-          auto log_of = [](const float4& f) { return f.y == INFINITY ? f.z : f.y; };
           float top = -INFINITY;  // the largest x of the row
           bool far = false;
 #pragma unroll 1
@@ -607,42 +643,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
               for (int k = 1; k < 16; ++k) x = fmaxf(x, __uint_as_float(v[u * 16 + k]));
               const float4 f = sc[c * 2 + u];
-              far |= f.y == INFINITY;
+              far |= f.z < 0.f;
               // -infinity stays where the factor is 0
-              top = fmaxf(top, x == -INFINITY ? x : fmaf(x, qs * f.x, log_of(f)));
+              top = fmaxf(top, x == -INFINITY ? x : fmaf(x, qs * f.x, f.y));
             }
           }
-          if (far && !wide) {
+          if (__builtin_expect(far && !wide, 0)) {
             wide = true;
             rmax = m;  // l is in units of 2^M so far
             settle(rmax, l, 0);
           }
-          if (wide) {  // l and R from the scores
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              const int here = seen - c * 32;
-              if (!__any_sync(0xffffffffu, here > 0)) break;
-              uint32_t v[32];
-              tmem_ld32(v, s_col + c * 32);
-              wait_ld();
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const float4 f = sc[c * 2 + u];
-                const int some = f.y == -INFINITY ? 0 : here - u * 16;  // a group that is not there
-                const float f1 = qs * f.x;
-                float x[16], most = -INFINITY;
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                  x[k] = k < some ? __uint_as_float(v[u * 16 + k]) * f1 : -INFINITY;
-                  most = fmaxf(most, x[k]);
-                }
-                const float r = fmaxf(rmax, most), from = r == -INFINITY ? 0.f : r;
-                l *= exp2_fast(rmax - from);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) l += exp2_fast(x[k] - from);
-                rmax = r;
-              }
-            }
+          if (__builtin_expect(wide, 0)) {  // l and R from the scores
+            const float2 y = sum_scores(sc, s_col, seen, qs, rmax, l);
+            rmax = y.x;
+            l = y.y;
           }
           const bool grow = top > m + kTopLog + 8.f;
           if (__any_sync(0xffffffffu, grow)) {
@@ -684,7 +698,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               for (int u = 0; u < 2; ++u) {
                 const float4 f = sc[c * 2 + u];
                 // not 0: a masked score stays -infinity (the largest, 2^29, times 1e-37 is nothing)
-                const float f1 = fmaxf(qs * f.x, 1e-37f), f0 = log_of(f) - base;
+                const float f1 = fmaxf(qs * f.x, 1e-37f), f0 = f.y - base;
                 float part = 0.f;
 #pragma unroll
                 for (int k = 0; k < 16; k += 2) {
@@ -798,7 +812,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (keys && lane < 2) {
           const float log_v = vs >= kTinyScale ? __log2f(vs) : -INFINITY;
           float4 f = make_float4(ks, log_v, __frcp_rn(vs), 0.f);
-          if (!is_near(vs)) f = make_float4(ks, INFINITY, log_v, 0.f);
+          if (!is_near(vs)) f.z = -INFINITY;
           if (!there) f = make_float4(0.f, -INFINITY, 0.f, 0.f);
           // four tiles of scales: the rows are done with those of tile j - 3 before the scores of
           // tile j - 2 are asked for, which the wait above has seen
