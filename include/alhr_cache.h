@@ -170,10 +170,12 @@ ALHR_API size_t alhr_attend_cache_workspace(const alhr_cache* cache,
  *   lse       device float [tokens][q_heads], or NULL
  *   workspace device, 16-byte aligned; used from launch to completion of this call, so calls that
  *             may run at the same time need one each
- * The sums are fp32; the result of a call depends on its inputs and the device alone. Requests
- * with more than 16 rows per key/value head are computed on the tensor core, whose waits are
- * bounded: should one run out (not expected), ALHR_DEVERR_TIMEOUT is set and out and lse of the
- * call are not to be used.
+ * The sums are fp32; a key's weight times its value scale is held in 16 bits: to 2^-11 of itself
+ * down to 2^-21 of the row's largest, below that to 2^-32 of the largest
+ * (alhr_attend_cache_selected holds it to 2^-22 of itself). The result of a call depends on its
+ * inputs and the device alone. Requests with more than 16 rows per key/value head are computed on the
+ * tensor core, whose waits are bounded: should one run out (not expected), ALHR_DEVERR_TIMEOUT is
+ * set and out and lse of the call are not to be used.
  */
 ALHR_API alhr_status alhr_attend_cache(const alhr_cache* cache, const alhr_cache_queries* queries,
                                        const void* Q, const int32_t* block_table,

@@ -5,7 +5,13 @@ namespace alhr {
 
 // Rows of one key head up to which a request is decoded (cache_decode.cu) and from which on it is
 // taken as a chunk (cache_chunk.cu): a key tile costs the chunk kernel the same for 1 to 128 rows,
-// the decoding one in proportion to groups of 16.
+// the decoding one in proportion to groups of 16. Measured, 16 requests of 16,384 int8 keys x 8 key
+// heads, microseconds of the one and the other kernel:
+//   rows        8          16         17 to 32     48         64         96         128
+//   d = 64      62 / 199   77 / 199   128 / 200    181 / 199  233 / 200  343 / 202  450 / 203
+//   d = 128     98 / 287   117 / 287  203 / 289    295 / 289  381 / 289  563 / 292  748 / 297
+// So they meet near 48 rows: at 17 to 47 the chunk kernel is the slower one, by 1.6 and 1.4 times
+// at 32, and neither is near the 41 and 82 us that the codes alone take.
 constexpr int kFewRows = 16;
 
 // max_rows: the most rows of one key head that a request may have.

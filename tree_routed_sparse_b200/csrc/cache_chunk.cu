@@ -7,10 +7,11 @@
 // What bounds it: the two products, 4 d flops a row and key, and one power of two a row and key; at
 // d = 128 the tensor core, the special-function unit and the operands' way through shared memory
 // need the same time (2048 cycles for 256 rows and 128 keys), at d = 64 the powers of two do. The
-// rows' own work is what it comes to: measured 1.12 ms for 2 x 2048 rows x 32 heads behind 14,336
-// keys at d = 128 (920 TFLOP/s, 0.56 of the measured bf16 rate; the tensor core works 41 % of the
-// time, the special-function unit 43 %), 0.97 with the rows' work alone. Score columns for each half
-// of a key tile, so that scores never wait for weights, took 1.15 ms.
+// rows' own work is what it comes to: measured 1.14 ms for 2 x 2048 rows x 32 heads behind 14,336
+// keys at d = 128 (904 TFLOP/s, 0.55 of the measured bf16 rate; the tensor core works 41 % of the
+// time, the special-function unit 43 %), 0.97 with the rows' work alone (when the whole took 1.12).
+// Score columns for each half of a key tile, so that scores never wait for weights, took 1.15 ms then.
+// Units whose value scales are not near 1 take 2.4 ms in this case (three passes over the scores).
 //
 // One CTA a multiprocessor takes 256 query rows (two tiles of 128) of one key head and walks key
 // tiles of 128. Eight warps load codes to registers, widen them to halves (exact) and write them to
@@ -20,7 +21,7 @@
 // for its products, S_i = Q_i K^T into tensor memory and O_i += P_i V with P_i read from tensor
 // memory, where the rows' threads put it in place of S_i. While the tensor core works on one tile
 // of rows the threads of the other one take their powers of two. A warp of its own for the products
-// was slower (1.14 ms): it has to be woken twice a tile. Rows of a request are (token, head of the
+// was slower (1.15 ms against 1.11): it has to be woken twice a tile. Rows of a request are (token, head of the
 // group) pairs, so that grouped heads share every key tile.
 //
 // As in cache_decode.cu the key tiles of all units form one list of which every CTA takes an
@@ -899,7 +900,9 @@ cudaError_t chunk_as(const AttendArgs& a, int sms, int row_limit, cudaStream_t s
 size_t chunk_workspace(int sms, int d) { return join_bytes(sms, kRows, d); }
 
 // Requests of more than row_limit rows (of one key head); the join has to follow. The kernel may
-// run beside the previous one of the stream, whose results it does not read, and ends behind it.
+// begin before the previous one of the stream has ended, whose results it does not read, and ends
+// behind it. A CTA of either fills a multiprocessor (198 KB of shared memory, 65,536 registers), so
+// only the one's end and the other's start overlap.
 cudaError_t launch_chunk(const AttendArgs& a, int d, int code, int sms, int row_limit,
                          cudaStream_t st) {
   if (d == 64)

@@ -11,9 +11,11 @@
 // out = 2^(M - R) O / l: a head of zeros takes the second power of two for every key.
 //
 // What bounds it: the codes have to be read once, 2 d bytes a key and head; everything else is
-// there to keep the memory busy (64 sequences of up to 16,384 int8 keys, 32 query heads over 8, d =
-// 128: 190 us, 6.2 TB/s; 4 sequences x 8 heads x 262,144 e4m3 keys: 341 us, 6.3 TB/s; 0.94 and 0.96
-// of the copy rate). The tiles of all (request, key head, row group)
+// there to keep the memory busy. Replayed from a graph: 64 sequences of up to 16,384 int8 keys, 32
+// query heads over 8, d = 128: 191 us, 6.2 TB/s; 4 sequences x 8 heads x 262,144 e4m3 keys: 342 us, 6.3
+// TB/s; 0.94 and 0.96 of the copy rate (both inputs are larger than L2). One call at a time for
+// seconds, at lower clocks: 216 and 334 us. With every value scale at 2^-100 (second powers of two):
+// 213 and 323 us. The tiles of all (request, key head, row group)
 // units form one list, and each warp of the GPU takes an equal, contiguous piece of it: no unit is
 // too short or too long, and no warp waits for another one. A warp copies its tiles (32 keys at d =
 // 128, 64 at d = 64: 8 KB) kStages ahead into its own piece of shared memory, 192 KB of copies in

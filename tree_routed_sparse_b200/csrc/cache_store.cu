@@ -1,9 +1,11 @@
 // cache_store.cu -- new tokens into the paged 8-bit cache, and its numbers back.
 //
 // Both are bound by memory: a stored number is read once (2 bytes) and written once (1 byte), a
-// loaded one the other way round. Measured, keys and values of 17.9 K tokens x 8 heads, d = 128, e4m3
-// blocks of 16, stored and read back: 51 us (4.3 TB/s, 0.66 of the copy rate). One appended token of
-// 64 sequences, stored and its blocks read back: 7.2 us, two launches.
+// loaded one the other way round. Measured (replayed from a graph, L2 warm), keys and values of 17.9 K
+// tokens x 8 heads, d = 128, e4m3 blocks of 16: 29 us stored, 25 us read back, 52 us together (4.3
+// TB/s, 0.65 of the copy rate). One appended token of 64 sequences, int8 blocks of 64: 3.1 us where no
+// block's scale grows, 10.3 us where every one's does (up to 63 rows a block are read and written
+// again, one pass behind the other), and 3.6 us for reading the blocks back.
 //
 // store: one warp takes one run (rows of consecutive slots of one block) of one head, keys or
 // values: the run's largest magnitude, the block's new scale, the codes of the rows before the run
@@ -273,7 +275,14 @@ __global__ void __launch_bounds__(256) load_kernel(const LoadArgs a) {
 
 template <int D, int CODE, int T>
 cudaError_t store_as(const StoreArgs& a, cudaStream_t st) {
-  // one token a warp while that leaves the GPU room (each may be a run of its own), else 16
+  // One token a warp while that leaves the GPU room (each may be a run of its own), else 16. Neither
+  // is the better one for every call of a size. Microseconds at one token and at 16 a warp, 8 heads,
+  // d = 128, bf16 into int8 blocks of 64, by the number of tokens:
+  //                                512          1024         2048         4096         large
+  //   one token a sequence         8.2 / 26.2   13.4 / 27.1  25.2 / 29.4  47.8 / 56.2  93.5 / 86.1 (8192)
+  //   whole blocks                 13.3 / 12.3  15.6 / 12.8  20.5 / 18.2  28.2 / 23.0  87.7 / 44.6 (16,384)
+  // The step lies at 1024 tokens of 8 heads: single tokens behind it pay for the prompts (27 us for
+  // 14.6 at 1100).
   const long long warps = static_cast<long long>(a.tokens) * a.c.heads * 2;
   const int per = warps <= 16384 ? 1 : 16;
   const dim3 grid(static_cast<unsigned>((a.tokens + per - 1) / per),
