@@ -10,8 +10,8 @@
 // rows' own work is what it comes to: measured 1.14 ms for 2 x 2048 rows x 32 heads behind 14,336
 // keys at d = 128 (904 TFLOP/s, 0.55 of the measured bf16 rate; the tensor core works 41 % of the
 // time, the special-function unit 43 %), 0.97 with the rows' work alone (when the whole took 1.12).
-// Score columns for each half of a key tile, so that scores never wait for weights, took 1.15 ms then.
-// Units whose value scales are not near 1 take 2.4 ms in this case (three passes over the scores).
+// Score columns for each half of a key tile, so that scores never wait for weights, took 1.15 ms
+// then. Units whose value scales are not near 1 take 2.4 ms in this case (three passes over the scores).
 //
 // One CTA a multiprocessor takes 256 query rows (two tiles of 128) of one key head and walks key
 // tiles of 128. Eight warps load codes to registers, widen them to halves (exact) and write them to
@@ -21,8 +21,8 @@
 // for its products, S_i = Q_i K^T into tensor memory and O_i += P_i V with P_i read from tensor
 // memory, where the rows' threads put it in place of S_i. While the tensor core works on one tile
 // of rows the threads of the other one take their powers of two. A warp of its own for the products
-// was slower (1.15 ms against 1.11): it has to be woken twice a tile. Rows of a request are (token, head of the
-// group) pairs, so that grouped heads share every key tile.
+// was slower (1.15 ms against 1.11): it has to be woken twice a tile. Rows of a request are (token,
+// head of the group) pairs, so that grouped heads share every key tile.
 //
 // As in cache_decode.cu the key tiles of all units form one list of which every CTA takes an
 // equal, contiguous piece; units that span pieces leave partial sums that a second kernel joins.
