@@ -184,6 +184,14 @@ def test_binding_refuses_what_it_cannot_pass_on(C):
             C._rows(bad, (4, 2, 64), torch.float32, "K", cpu)
 
 
+@pytest.mark.parametrize("tokens", [-1, 2 ** 31, 2 ** 32, 2 ** 32 + 4])
+def test_plan_refuses_tokens_that_32_bits_do_not_hold(C, tokens):
+    """The ABI's count is an int32: a larger one is named, not cut to its low bits."""
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    with pytest.raises(ValueError, match="tokens"):
+        C.plan_blocks(i32(2), i32(2), i32(2, 3), i32(4), i32(1), tokens, 16)
+
+
 def test_plan_by_hand():
     """The test oracle itself: two requests, pages of 4 written out by hand."""
     from cache_util import plan_ref

@@ -134,13 +134,13 @@ def plan_blocks(ctx_len: torch.Tensor, new_len: torch.Tensor, block_table: torch
     blocks: the cache's (a larger block number is refused on the device). Returns q_start int32
     [R + 1], seq_len int32 [R], slots int64 [tokens], positions int32 [tokens] and free_next
     int32 [1], the next step's free_first."""
+    tokens = int(tokens)
+    if not 0 <= tokens < 2**31:  # an int32 of the ABI
+        raise ValueError(f"tokens {tokens}: at least 0, below 2^31")
     dev = _cuda(block_table, "block_table")
     if block_table.dim() != 2 or free_blocks.dim() != 1:
         raise ValueError("block_table [requests, max_blocks] and free_blocks [free] expected")
     r, width = block_table.shape
-    tokens = int(tokens)
-    if tokens < 0:
-        raise ValueError(f"tokens {tokens}: at least 0")
     ctx = _need(ctx_len, torch.int32, (r,), "ctx_len", dev)
     new = _need(new_len, torch.int32, (r,), "new_len", dev)
     table = _need(block_table, torch.int32, (r, width), "block_table", dev)
